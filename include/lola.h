@@ -30,7 +30,8 @@
  *   - Feature map phi(x) = [softmax(x W_g), softmax(-x W_g)] (Hedgehog form,
  *     fixed by this library; the pages leave phi as "learned"), D = 2 Dh.
  *   - Sequences of a batch advance in lock step: every call processes the
- *     same number of tokens for all B sequences.
+ *     same number of tokens for all B sequences (or for the number chosen
+ *     with lola_set_batch or lola_state_fork).
  *   - Precision: SRE, selection, fold and the state are f32.  With bf16
  *     inputs the prefill output runs Q K^T in bf16 and P V in f16 on the
  *     tensor cores (f32 accumulation), so values v must satisfy |v| < 65504;
@@ -237,11 +238,91 @@ int lola_sre_map(lola_state* st, const void* k, const void* v, int T, float* sre
  * error, LOLA_OK otherwise. */
 int lola_state_check(lola_state* st, void* stream);
 
+/* Number of sequences that later calls process: the first n of the config's B
+ * (q, k, v and y then have n sequences).  Only while no token has been
+ * processed; init and reset set it to B, lola_state_fork sets it later.
+ * LOLA_ERR_INVALID_ARG otherwise or for n outside 1..B.  With n = 1 a prompt
+ * that many samples share is prefilled once and then forked in place. */
+int lola_set_batch(lola_state* st, int n);
+
+/* Copy whole sequences (no counterpart in the paper; the memories are those of
+ * notes §2.4, Fig. 1): sequence b of dst, b < n, becomes a copy of sequence
+ * parents[b] of src: H, s, the cache, the window and what decode keeps beside
+ * them.  dst then holds n sequences at src's position t and ranks by src's
+ * scoring rule; its W and its read options stay.  Samples of a prompt
+ * (several b with one parent), the survivors of a beam search (dst == src,
+ * any repetitions and cycles) and dropping finished sequences (n smaller) are
+ * all forks.  parents: device int32 [n], read on the stream; each in
+ * [0, sequences of src).  One that is not leaves its sequence's memories
+ * unwritten and makes lola_state_check return LOLA_ERR_INVALID_ARG until dst
+ * is reset (the call itself does not wait for the device).  A device timeout recorded in src is recorded in dst too.
+ * dst and src must agree in Hq, Hkv, d, Dh, eta, lambda and dtype (B, chunk and
+ * max_tokens may differ) and live on the current device; n is 1..B of dst, at
+ * most 1500 in place (LOLA_ERR_UNSUPPORTED).  Enqueued on `stream`, which must
+ * be ordered after earlier work on both states.  A prefill or decode step may
+ * follow; lola_sre_map and the trace need a new prefill call first.
+ * Bound: HBM; each distinct parent read once, each sequence written once. */
+int lola_state_fork(lola_state* dst, const lola_state* src, const int* parents, int n, void* stream);
+
+/* Exact (softmax) attention beside the hybrid layer, stateless: for the encoder
+ * of an encoder-decoder model and for the exact layers of a stack whose other
+ * layers are hybrid.  Row (b, t, h) of the queries reads kv head h / (Hq / Hkv):
+ *   y[b][t][h] = sum_i p_i v_i,   p = softmax over its keys i of scale q . k_i,
+ *   lse[b][t][h] = log sum_i exp(scale q . k_i)   (natural log).
+ * A row that reads no key gets y = 0 and lse = -infinity.  Keys that a row does
+ * not read never reach its result, whatever they hold (NaN and infinities too).
+ * y is in dtype (its next use is a projection in that type), lse float32.
+ * Precision: bf16 inputs multiply on the tensor cores with f32 accumulation;
+ * f32 inputs, the softmax statistics and the sums are f32.
+ *
+ * Sizes: B, T >= 1; P, L >= 0; Hq % Hkv == 0; d in {64, 128}; scale > 0 and
+ * finite; B, Hkv <= 65535; B * T * Hq < 2^31.  Strides are in elements (batch, token, head;
+ * the d elements of a head are contiguous) and non-negative, multiples of 16
+ * bytes; q, k, v and y are 16-byte aligned.  A batch or head stride may be 0
+ * (one tensor for all); the token stride of more than one key may not. */
+typedef struct lola_attn_config {
+    int B;                  /* sequences                                              */
+    int T;                  /* query tokens of each                                   */
+    int Hq, Hkv, d;         /* heads and head dimension                               */
+    int dtype;              /* LOLA_DTYPE_* of q, k, v, y                             */
+    int P;                  /* keys that all sequences share (prefix attention)       */
+    int L;                  /* keys of each sequence: its own, or the encoder's       */
+    float scale;            /* 1 / sqrt(d) in most models                             */
+    long long q_stride[3];  /* batch, token, head                                     */
+    long long kp_stride[2]; /* shared keys and values: token, head                    */
+    long long vp_stride[2];
+    long long k_stride[3];  /* each sequence's keys and values: batch, token, head    */
+    long long v_stride[3];
+} lola_attn_config;
+
+/* Bytes of scratch that the two calls below need with this configuration (may
+ * be 0).  The caller owns it, 256-byte aligned; its contents mean nothing
+ * between calls.  Calls that may run at the same time need one each. */
+int lola_attn_workspace(const lola_attn_config* cfg, size_t* bytes);
+
+/* Attention to an encoder's states of another length: q [B][T][Hq][d], k and v
+ * [B][L][Hkv][d]; every query of sequence b reads keys s < kv_len[b] (device
+ * int32 [B]; values are clamped to 0..L; NULL: L for every sequence).  P must be
+ * 0.  y [B][T][Hq][d] contiguous; lse [B][T][Hq] or NULL. */
+int lola_cross_attention(const lola_attn_config* cfg, const void* q, const void* k, const void* v,
+                         const int* kv_len, void* y, float* lse, void* workspace, size_t bytes, void* stream);
+
+/* Attention of sequences that share a prefix of P keys (k_prefix, v_prefix
+ * [P][Hkv][d]; read once for the whole batch), each followed by keys of its own
+ * (k, v [B][L][Hkv][d], of which sequence b has own_len[b]; device int32 [B],
+ * clamped to 0..L; NULL: L).  The T queries are the last T tokens of their
+ * sequence and causal in it: query t reads the prefix and its own keys
+ * s <= own_len[b] - T + t (none of its own where that is negative).  With T = 1
+ * this is a decode step of B samples of one prompt. */
+int lola_prefix_attention(const lola_attn_config* cfg, const void* q, const void* k_prefix, const void* v_prefix,
+                          const void* k, const void* v, const int* own_len, void* y, float* lse, void* workspace,
+                          size_t bytes, void* stream);
+
 /* Fill *out with device views of the state (no copy, no synchronisation). */
 int lola_state_export(const lola_state* st, lola_state_view* out);
 
 /* Tracing aid.  Kernel classes, in this order: 0 feature map, 1 scan (memory
- * update chain), 2 output, 3 finalize, 4 decode, 5 SRE map, 6 window scores of
+ * update chain), 2 output, 3 finalize (and forks), 4 decode, 5 SRE map, 6 window scores of
  * an alternative scoring rule.  While enabled, every kernel
  * launch of `st` is bracketed by CUDA events recorded on its stream.
  * lola_profile_read waits for those events, adds their elapsed times (ms) and

@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, byref, c_int, c_longlong, c_size_t, c_void_p, c_char_p
+from ctypes import POINTER, byref, c_float, c_int, c_longlong, c_size_t, c_void_p, c_char_p
 
 import torch
 
@@ -19,6 +19,7 @@ LIB_PATH = os.path.join(_HERE, "liblola.so")
 
 DTYPE_F32, DTYPE_BF16 = 0, 1
 _TORCH_DTYPE = {DTYPE_F32: torch.float32, DTYPE_BF16: torch.bfloat16}
+_DTYPE_CODE = {t: c for c, t in _TORCH_DTYPE.items()}
 ERRORS = {0: "OK", -1: "INVALID_ARG", -2: "BUF_TOO_SMALL", -3: "CUDA", -4: "TIMEOUT", -5: "UNSUPPORTED"}
 
 # Every entry point of include/lola.h.
@@ -27,6 +28,8 @@ EXPORTS = ("lola_state_bytes", "lola_state_init", "lola_state_reset", "lola_stat
            "lola_decode_step_host", "lola_state_export", "lola_profile_enable",
            "lola_profile_read", "lola_launch_count", "lola_prefill_once_noalloc", "lola_selftest_umma",
            "lola_set_read_options", "lola_sre_map", "lola_set_scorer", "lola_state_check",
+           "lola_set_batch", "lola_state_fork", "lola_attn_workspace", "lola_cross_attention",
+           "lola_prefix_attention",
            "lola_last_error_string")
 KERNEL_CLASSES = ("phi", "scan", "output", "finalize", "decode", "sre_map", "scores")
 READ_HIDE_STATE, READ_HIDE_SPARSE = 1, 2
@@ -45,6 +48,13 @@ class LolaStateView(ctypes.Structure):
                 ("cache_pos", c_void_p), ("win_k", c_void_p), ("win_v", c_void_p),
                 ("win_phik", c_void_p), ("trace_pos", c_void_p), ("trace_len", c_int),
                 ("trace_stride", c_int), ("trace_t0", c_longlong), ("err_word", c_void_p)]
+
+
+class LolaAttnConfig(ctypes.Structure):
+    _fields_ = [("B", c_int), ("T", c_int), ("Hq", c_int), ("Hkv", c_int), ("d", c_int), ("dtype", c_int),
+                ("P", c_int), ("L", c_int), ("scale", c_float), ("q_stride", c_longlong * 3),
+                ("kp_stride", c_longlong * 2), ("vp_stride", c_longlong * 2), ("k_stride", c_longlong * 3),
+                ("v_stride", c_longlong * 3)]
 
 
 class LolaError(RuntimeError):
@@ -80,6 +90,11 @@ def lib() -> ctypes.CDLL:
     L.lola_sre_map.argtypes = [vp, vp, vp, c_int, vp, vp, vp]
     L.lola_set_scorer.argtypes = [vp, c_int]
     L.lola_state_check.argtypes = [vp, vp]
+    L.lola_set_batch.argtypes = [vp, c_int]
+    L.lola_state_fork.argtypes = [vp, vp, vp, c_int, vp]
+    L.lola_attn_workspace.argtypes = [POINTER(LolaAttnConfig), POINTER(c_size_t)]
+    L.lola_cross_attention.argtypes = [POINTER(LolaAttnConfig), vp, vp, vp, vp, vp, vp, vp, c_size_t, vp]
+    L.lola_prefix_attention.argtypes = [POINTER(LolaAttnConfig), vp, vp, vp, vp, vp, vp, vp, vp, vp, c_size_t, vp]
     L.lola_launch_count.argtypes = []
     L.lola_launch_count.restype = c_longlong
     L.lola_last_error_string.argtypes = []
@@ -136,6 +151,111 @@ def _stream(stream=None) -> c_void_p:
     return c_void_p(s.cuda_stream)
 
 
+# -- exact attention beside the layer ---------------------------------------------
+def _attn_tensor(x, name, shape, dtype, device, packed=False):
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if tuple(x.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(x.shape)}, expected {tuple(shape)}")
+    if x.dtype != dtype:
+        raise ValueError(f"{name}: dtype {x.dtype}, expected {dtype}")
+    if x.device != device:
+        raise ValueError(f"{name}: on {x.device}, expected {device}")
+    if packed and not x.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if not packed and x.numel() and x.stride(-1) != 1:
+        raise ValueError(f"{name}: the head's elements must be contiguous (last stride 1)")
+
+
+def _attention(entry, q, kp, vp, k, v, lens, lens_name, scale, y, lse, workspace, stream):
+    for x, name in ((q, "q"), (k, "k")):
+        if not isinstance(x, torch.Tensor) or x.dim() != 4:
+            raise TypeError(f"{name} must be a torch.Tensor of 4 dimensions")
+    if not q.is_cuda:
+        raise ValueError(f"q: on {q.device}, expected a CUDA device")
+    if q.dtype not in _DTYPE_CODE:
+        raise ValueError(f"q: dtype {q.dtype}, expected one of {list(_DTYPE_CODE)}")
+    B, T, Hq, d = q.shape
+    L, Hkv = k.shape[1], k.shape[2]
+    dev, dt = q.device, q.dtype
+    _attn_tensor(q, "q", (B, T, Hq, d), dt, dev)
+    _attn_tensor(k, "k", (B, L, Hkv, d), dt, dev)
+    _attn_tensor(v, "v", (B, L, Hkv, d), dt, dev)
+    P = 0
+    if kp is not None:
+        if not isinstance(kp, torch.Tensor) or kp.dim() != 3:
+            raise TypeError("k_prefix must be a torch.Tensor of 3 dimensions")
+        P = kp.shape[0]
+        _attn_tensor(kp, "k_prefix", (P, Hkv, d), dt, dev)
+        _attn_tensor(vp, "v_prefix", (P, Hkv, d), dt, dev)
+    if lens is not None:
+        _attn_tensor(lens, lens_name, (B,), torch.int32, dev, packed=True)
+    if y is not None:
+        _attn_tensor(y, "y", (B, T, Hq, d), dt, dev, packed=True)
+    if lse is not None:
+        _attn_tensor(lse, "lse", (B, T, Hq), torch.float32, dev, packed=True)
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"stream: on {stream.device}, expected {dev}")
+    c = LolaAttnConfig(B, T, Hq, Hkv, d, _DTYPE_CODE[dt], P, L, d ** -0.5 if scale is None else scale,
+                       q.stride()[:3], kp.stride()[:2] if P else (0, 0), vp.stride()[:2] if P else (0, 0),
+                       k.stride()[:3], v.stride()[:3])
+    L_ = lib()
+    n = c_size_t()
+    _check(L_.lola_attn_workspace(byref(c), byref(n)))
+    # allocated on the call's own device and stream, so that the allocator orders their reuse after it
+    with torch.cuda.device(dev), torch.cuda.stream(stream):
+        if y is None:
+            y = torch.empty((B, T, Hq, d), dtype=dt, device=dev)
+        if workspace is None:
+            workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
+        elif not (isinstance(workspace, torch.Tensor) and workspace.dtype == torch.uint8 and workspace.device == dev
+                  and workspace.is_contiguous()):
+            raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
+        args = [q.data_ptr()] + ([kp.data_ptr(), vp.data_ptr()] if kp is not None else [])
+        args += [k.data_ptr(), v.data_ptr(), None if lens is None else lens.data_ptr(), y.data_ptr(),
+                 None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                 torch.cuda.current_stream(dev).cuda_stream]
+        _check(getattr(L_, entry)(byref(c), *args))
+    return y
+
+
+def attention_workspace(q, k, k_prefix=None) -> int:
+    """Bytes of scratch that cross_attention(q, k, ...) or prefix_attention(q, k_prefix, ..., k, ...) uses."""
+    c = LolaAttnConfig(q.shape[0], q.shape[1], q.shape[2], k.shape[2], q.shape[3], _DTYPE_CODE[q.dtype],
+                       0 if k_prefix is None else k_prefix.shape[0], k.shape[1], 1.0)
+    unit = 16 // q.element_size()                    # (strides do not matter here)
+    for f in ("q_stride", "kp_stride", "vp_stride", "k_stride", "v_stride"):
+        for i in range(len(getattr(c, f))):
+            getattr(c, f)[i] = unit
+    n = c_size_t()
+    _check(lib().lola_attn_workspace(byref(c), byref(n)))
+    return n.value
+
+
+def cross_attention(q, k, v, kv_len=None, scale=None, y=None, lse=None, workspace=None, stream=None):
+    """Attention to an encoder's states: q [B,T,Hq,d], k/v [B,S,Hkv,d] -> y [B,T,Hq,d] in q's dtype.
+
+    Every query of sequence b reads the keys s < kv_len[b] (int32 [B] on the device; all S if
+    None).  scale is 1/sqrt(d) if None.  Any strides with contiguous heads, a batch stride of 0
+    (one encoder output for all sequences, read once) among them.  lse (float32 [B,T,Hq]), if
+    given, receives each row's log-sum-exp.  workspace: scratch to use instead of an allocation
+    (attention_workspace bytes); calls that may overlap need one each."""
+    return _attention("lola_cross_attention", q, None, None, k, v, kv_len, "kv_len", scale, y, lse, workspace, stream)
+
+
+def prefix_attention(q, k_prefix, v_prefix, k, v, own_len=None, scale=None, y=None, lse=None, workspace=None,
+                     stream=None):
+    """Attention of a batch that shares a prefix, which is read once for all its sequences.
+
+    q [B,T,Hq,d]: the last T tokens of each sequence; k_prefix/v_prefix [P,Hkv,d]; k/v
+    [B,L,Hkv,d]: each sequence's own keys, own_len[b] of them (int32 [B]; all L if None).  Query
+    t reads the prefix and its own keys s <= own_len[b] - T + t.  The rest as cross_attention."""
+    if k_prefix is None or v_prefix is None:
+        raise TypeError("k_prefix and v_prefix must be torch.Tensors")
+    return _attention("lola_prefix_attention", q, k_prefix, v_prefix, k, v, own_len, "own_len", scale, y, lse,
+                      workspace, stream)
+
+
 class LolaLayer:
     """One LoLA attention layer state bound to a caller-owned device buffer.
 
@@ -147,7 +267,7 @@ class LolaLayer:
         self.device = torch.device(device)
         self.dtype = _TORCH_DTYPE[cfg.dtype]
         self.D = 2 * cfg.Dh
-        self.S = cfg.B * cfg.Hkv
+        self.B = cfg.B                      # sequences that calls process (set_batch, fork)
         self._check_tensor(W, (cfg.Hkv, cfg.d, cfg.Dh), self.dtype, "W")
         self.nbytes = state_bytes(cfg)
         self.buf = torch.empty(self.nbytes + 256, dtype=torch.uint8, device=self.device)
@@ -156,6 +276,11 @@ class LolaLayer:
         _check(lib().lola_state_init(byref(cfg), c_void_p(W.data_ptr()),
                                      c_void_p(self.buf.data_ptr() + self._off), self.nbytes,
                                      _stream(stream), byref(self.handle)))
+
+    @property
+    def S(self) -> int:
+        """Streams (sequences x kv heads) that calls process."""
+        return self.B * self.cfg.Hkv
 
     # -- argument checks (marshalling only) --------------------------------
     def _check_tensor(self, x, shape, dtype, name, device=None):
@@ -173,10 +298,10 @@ class LolaLayer:
             raise ValueError(f"{name} must be contiguous")
 
     def _shapes(self, T):
-        c = self.cfg
+        c, B = self.cfg, self.B
         if T is None:
-            return (c.B, c.Hq, c.d), (c.B, c.Hkv, c.d)
-        return (c.B, T, c.Hq, c.d), (c.B, T, c.Hkv, c.d)
+            return (B, c.Hq, c.d), (B, c.Hkv, c.d)
+        return (B, T, c.Hq, c.d), (B, T, c.Hkv, c.d)
 
     # -- calls --------------------------------------------------------------
     def prefill(self, q, k, v, y=None, stream=None) -> torch.Tensor:
@@ -238,6 +363,28 @@ class LolaLayer:
         """Hide memory branches from later reads (READ_HIDE_* bits); update-first decode order."""
         _check(lib().lola_set_read_options(self.handle, int(read_mask), 1 if decode_update_first else 0))
 
+    def set_batch(self, n: int) -> None:
+        """Process only the first n sequences; only before the first token."""
+        _check(lib().lola_set_batch(self.handle, int(n)))
+        self.B = int(n)
+
+    def fork(self, parents: torch.Tensor, src: "LolaLayer | None" = None, stream=None) -> None:
+        """Sequence b becomes a copy of sequence parents[b] of `src` (of this layer itself if None).
+
+        parents: int32 [n] on the layer's device; the layer then holds n sequences.  A parent
+        outside src's sequences is reported by check()."""
+        src = self if src is None else src
+        if not isinstance(src, LolaLayer):
+            raise TypeError("src must be a LolaLayer")
+        if not isinstance(parents, torch.Tensor) or parents.dim() != 1:
+            raise TypeError("parents must be a 1-d torch.Tensor")
+        n = parents.shape[0]
+        self._check_tensor(parents, (n,), torch.int32, "parents", device=self.buf.device)
+        if src.buf.device != self.buf.device:
+            raise ValueError(f"src is on {src.buf.device}, expected {self.buf.device}")
+        _check(lib().lola_state_fork(self.handle, src.handle, c_void_p(parents.data_ptr()), n, _stream(stream)))
+        self.B = n
+
     def set_scorer(self, scorer) -> None:
         """Scoring rule (a name from SCORERS or its LOLA_SCORE_* number); only before the first token."""
         code = SCORERS.index(scorer) if isinstance(scorer, str) else int(scorer)
@@ -253,7 +400,7 @@ class LolaLayer:
         self._check_tensor(v, sk, self.dtype, "v")
         v_ = LolaStateView()
         _check(lib().lola_state_export(self.handle, byref(v_)))
-        shape = (c.B, c.Hkv, max(v_.trace_len, 1), T)
+        shape = (self.B, c.Hkv, max(v_.trace_len, 1), T)
         if sre is None:
             sre = torch.empty(shape, dtype=torch.float32, device=self.device)
         if rel is None:
@@ -283,6 +430,7 @@ class LolaLayer:
 
     def reset(self, stream=None) -> None:
         _check(lib().lola_state_reset(self.handle, _stream(stream)))
+        self.B = self.cfg.B
 
     # -- state views ----------------------------------------------------------
     def _view(self, ptr, shape, dtype):

@@ -89,14 +89,19 @@ cudaError_t traced(lola_state* st, int cls, int kernels, cudaStream_t s, F&& lau
     return e;
 }
 
+int vfail(int code, const char* fmt, va_list ap) {
+    char buf[512];
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    g_err = buf;
+    return code;
+}
+
 int fail(int code, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
 int fail(int code, const char* fmt, ...) {
-    char buf[512];
     va_list ap;
     va_start(ap, fmt);
-    vsnprintf(buf, sizeof buf, fmt, ap);
+    vfail(code, fmt, ap);
     va_end(ap);
-    g_err = buf;
     return code;
 }
 
@@ -186,6 +191,13 @@ lola::StatePtrs state_ptrs(const lola_state* st) {
     return p;
 }
 
+// The sequences that calls process: the first B of the cfg.B the buffer holds (every
+// per-stream array is stream-major, so the layout does not depend on B).
+void set_sequences(lola_state* st, int B) {
+    st->dm.B = B;
+    st->dm.S = B * st->dm.Hkv;
+}
+
 int clear_state(lola_state* st, cudaStream_t s) {
     const lola::Dims& dm = st->dm;
     const lola::Layout& L = st->L;
@@ -193,8 +205,9 @@ int clear_state(lola_state* st, cudaStream_t s) {
     cudaError_t e = cudaMemsetAsync(st->base + L.H, 0, L.phik_new - L.H, s);
     if (e == cudaSuccess) e = cudaMemsetAsync(st->base + L.err, 0, 256, s);
     if (e == cudaSuccess && dm.lam > 0)
-        e = cudaMemsetAsync(st->base + L.cache_pos, 0xFF, (size_t)dm.S * dm.lam * 4, s);
+        e = cudaMemsetAsync(st->base + L.cache_pos, 0xFF, (size_t)st->cfg.B * dm.Hkv * dm.lam * 4, s);
     if (e != cudaSuccess) return cuda_fail(e, "clearing the state");
+    set_sequences(st, st->cfg.B);
     st->t = 0;
     st->last_nc = -1;
     st->last_t0 = 0;
@@ -205,6 +218,17 @@ int clear_state(lola_state* st, cudaStream_t s) {
 bool misaligned(const void* p) { return ((uintptr_t)p & 15u) != 0; }
 
 }  // namespace
+
+namespace lola {
+int report(int code, const char* fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    vfail(code, fmt, ap);
+    va_end(ap);
+    return code;
+}
+void count_launches(int kernels) { g_launches += kernels; }
+}  // namespace lola
 
 extern "C" {
 
@@ -332,6 +356,76 @@ int lola_set_read_options(lola_state* st, int read_mask, int decode_update_first
         return fail(LOLA_ERR_INVALID_ARG, "decode_update_first=%d must be 0 or 1", decode_update_first);
     st->read_mask = read_mask;
     st->update_first = decode_update_first;
+    return LOLA_OK;
+}
+
+int lola_set_batch(lola_state* st, int n) {
+    if (!st) return fail(LOLA_ERR_INVALID_ARG, "null state");
+    if (n < 1 || n > st->cfg.B) return fail(LOLA_ERR_INVALID_ARG, "n=%d sequences (1..%d)", n, st->cfg.B);
+    if (st->t != 0 && n != st->dm.B)
+        return fail(LOLA_ERR_INVALID_ARG, "the number of sequences can be set only before the first token "
+                    "(after lola_state_init or lola_state_reset); later lola_state_fork chooses it");
+    set_sequences(st, n);
+    return LOLA_OK;
+}
+
+int lola_state_fork(lola_state* dst, const lola_state* src, const int* parents, int n, void* stream) {
+    if (!dst || !src || !parents) return fail(LOLA_ERR_INVALID_ARG, "null argument");
+    if ((uintptr_t)parents & 3) return fail(LOLA_ERR_INVALID_ARG, "parents must be 4-byte aligned");
+    const lola_config &cd = dst->cfg, &cs = src->cfg;
+    if (n < 1 || n > cd.B) return fail(LOLA_ERR_INVALID_ARG, "n=%d sequences (1..%d of the destination)", n, cd.B);
+    if (cd.Hq != cs.Hq || cd.Hkv != cs.Hkv || cd.d != cs.d || cd.Dh != cs.Dh || cd.eta != cs.eta ||
+        cd.lambda != cs.lambda || cd.dtype != cs.dtype)
+        return fail(LOLA_ERR_INVALID_ARG, "the two states differ in Hq, Hkv, d, Dh, eta, lambda or dtype");
+    if (dst == src && n > lola::kForkInPlaceMax)
+        return fail(LOLA_ERR_UNSUPPORTED, "n=%d > %d sequences in place (fork into another state)", n,
+                    lola::kForkInPlaceMax);
+    lola::ForkArgs a{};
+    const lola::Dims& dm = src->dm;
+    const lola::Layout &Ls = src->L, &Ld = dst->L;
+    auto add = [&](size_t from, size_t to, size_t stream_bytes) {
+        if (stream_bytes == 0) return;
+        lola::ForkSeg& sg = a.seg[a.nseg++];
+        sg.src = src->base + from;
+        sg.dst = dst->base + to;
+        sg.seq_bytes = (long long)stream_bytes * dm.Hkv;
+    };
+    const size_t lam = dm.lam, eta = dm.eta, e = dm.esize, D = dm.D, d = dm.d;
+    add(Ls.H, Ld.H, D * d * 4);
+    add(Ls.s, Ld.s, D * 4);
+    add(Ls.cache_k, Ld.cache_k, lam * d * e);
+    add(Ls.cache_v, Ld.cache_v, lam * d * e);
+    add(Ls.cache_phik, Ld.cache_phik, lam * D * 4);
+    add(Ls.cache_pos, Ld.cache_pos, lam * 4);
+    add(Ls.win_k, Ld.win_k, eta * d * e);
+    add(Ls.win_v, Ld.win_v, eta * d * e);
+    add(Ls.win_phik, Ld.win_phik, eta * D * 4);
+    // decode's per-slot residuals, while they match (H, s); the window scores of another rule
+    const bool sre = src->scorer == LOLA_SCORE_SRE;
+    if (sre && src->resid_ok) {
+        add(Ls.cache_R, Ld.cache_R, lam * d * 4);
+        add(Ls.cache_den, Ld.cache_den, lam * 4);
+    }
+    if (!sre || src->resid_ok) add(Ls.cache_sc, Ld.cache_sc, lam * 4);
+    if (!sre) add(Ls.win_sc, Ld.win_sc, eta * 4);
+    a.parents = parents;
+    a.n = n;
+    a.src_B = dm.B;
+    a.src_err = (int*)(src->base + Ls.err);
+    a.dst_err = (int*)(dst->base + Ld.err);
+    cudaStream_t s = (cudaStream_t)stream;
+    int dev = 0, sms = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (err != cudaSuccess) return cuda_fail(err, "reading the device");
+    err = traced(dst, 3, 1, s, [&] { return lola::launch_fork(a, sms, s); });
+    if (err != cudaSuccess) return cuda_fail(err, "fork kernel");
+    set_sequences(dst, n);
+    dst->t = src->t;
+    dst->scorer = src->scorer;
+    dst->resid_ok = src->resid_ok;
+    dst->last_nc = -1;        // the snapshots of the last prefill call do not describe the forked sequences
+    dst->last_t0 = 0;
     return LOLA_OK;
 }
 
@@ -622,6 +716,9 @@ int lola_state_check(lola_state* st, void* stream) {
     cudaError_t e = cudaMemcpyAsync(&word, st->base + st->L.err, sizeof(int), cudaMemcpyDeviceToHost, s);
     if (e == cudaSuccess) e = cudaStreamSynchronize(s);
     if (e != cudaSuccess) return cuda_fail(e, "reading the device error word");
+    if (word == 2)
+        return fail(LOLA_ERR_INVALID_ARG, "a fork's parent was outside the source's sequences; the sequences it "
+                    "should have filled are not valid: fork them again from a valid state, or reset");
     if (word != 0)
         return fail(LOLA_ERR_TIMEOUT, "a bounded device-side wait gave up (error word 0x%x); the results of "
                     "the calls since the last reset are not valid: reset the state", (unsigned)word);

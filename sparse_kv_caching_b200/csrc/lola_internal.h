@@ -106,7 +106,35 @@ struct SreMapArgs {
     int nc;                // its chunks
 };
 
+// One memory of a fork: rows of seq_bytes, one per sequence, gathered by the parents.
+struct ForkSeg {
+    const char* src;
+    char* dst;
+    long long seq_bytes;
+    long long cols, tile0; // columns per sequence and the memory's first tile (set by the launcher)
+    int wide;              // columns of 16 bytes (else 4)
+};
+constexpr int kForkSegs = 13;          // memories a fork may copy
+constexpr int kForkGroup = 16;         // destination sequences per CTA (between two states)
+constexpr int kForkInPlaceMax = 1500;  // sequences of an in-place fork (shared-memory slots, 32 threads x 4 bytes)
+
+struct ForkArgs {
+    ForkSeg seg[kForkSegs];
+    int nseg;
+    const int* parents;    // [n] device
+    int n, src_B;
+    int* src_err;
+    int* dst_err;          // bit 1: a parent outside [0, src_B)
+    long long tiles;       // set by the launcher
+    int tile_cols;
+};
+
+// Sets the text of lola_last_error_string and returns code; adds to lola_launch_count.
+int report(int code, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+void count_launches(int kernels);
+
 // Launchers (each returns cudaGetLastError() of its launch).
+cudaError_t launch_fork(ForkArgs a, int num_sms, cudaStream_t s);
 cudaError_t launch_phi_keys(const PrefillArgs& a, cudaStream_t s);
 cudaError_t launch_scan(const PrefillArgs& a, cudaStream_t s);
 // The chain on the tensor cores (scan_tc.cu); cudaErrorNotSupported outside its shapes.
