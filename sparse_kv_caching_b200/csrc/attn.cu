@@ -96,16 +96,93 @@ __global__ void __launch_bounds__(256) attn_kernel(const __grid_constant__ AttnA
     }
 }
 
-cudaError_t launch_attn(const AttnArgs& a, cudaStream_t s) {
-    const dim3 grid((a.T * a.Gq + kAtRows - 1) / kAtRows, a.Hkv, a.B);
-    const bool bf = a.dtype == 1;
-    if (a.d == 128) {
-        if (bf) attn_kernel<128, __nv_bfloat16><<<grid, 256, 0, s>>>(a);
-        else attn_kernel<128, float><<<grid, 256, 0, s>>>(a);
-    } else {
-        if (bf) attn_kernel<64, __nv_bfloat16><<<grid, 256, 0, s>>>(a);
-        else attn_kernel<64, float><<<grid, 256, 0, s>>>(a);
+// The parts of a row put together: with L_p the log2-sum-exp of part p and O_p its
+// normalised sum, L = log2 sum 2^L_p and y = sum 2^(L_p - L) O_p.  One warp per row;
+// the parts were just written and come from L2.
+template <int DIM, typename TOut>
+__global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ AttnArgs a) {
+    constexpr int EPL = DIM / 32;
+    const size_t rows = (size_t)a.B * a.T * a.Hq, row = (size_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (row >= rows) return;
+    const int np = a.parts_own + (a.walk ? 0 : a.parts_shared);
+    float m = -INFINITY;
+    for (int p = lane; p < np; p += 32) m = fmaxf(m, a.part_l[p * rows + row]);
+    m = warp_max(m);
+    const float ref = m == -INFINITY ? 0.f : m;
+    float sum = 0.f, acc[EPL];
+#pragma unroll
+    for (int u = 0; u < EPL; ++u) acc[u] = 0.f;
+#pragma unroll 4
+    for (int p = 0; p < np; ++p) {
+        const float w = exp2f(a.part_l[p * rows + row] - ref);
+        const float* o = a.part_o + (p * rows + row) * DIM + lane * EPL;
+        sum += w;
+        if (EPL == 4) {
+            const float4 x = *reinterpret_cast<const float4*>(o);
+            acc[0] = fmaf(w, x.x, acc[0]); acc[1] = fmaf(w, x.y, acc[1]);
+            acc[EPL - 2] = fmaf(w, x.z, acc[EPL - 2]); acc[EPL - 1] = fmaf(w, x.w, acc[EPL - 1]);
+        } else {
+            const float2 x = *reinterpret_cast<const float2*>(o);
+            acc[0] = fmaf(w, x.x, acc[0]); acc[1] = fmaf(w, x.y, acc[1]);
+        }
     }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+    for (int u = 0; u < EPL; ++u) store_as((TOut*)a.y + row * DIM + lane * EPL + u, acc[u] * inv);
+    if (a.lse && lane == 0) a.lse[row] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
+}
+
+size_t plan_attn(AttnArgs& a, int num_sms) {
+    a.walk = 1;
+    a.parts_shared = 0;
+    a.parts_own = 1;
+    a.chunk_shared = a.chunk_own = 0;
+    const int rows = a.T * a.Gq;
+    const long long keys = (long long)a.shared.n + a.own.n, ctas = (long long)a.B * a.Hkv;
+    auto cut = [&](long long n, long long ctas, int* parts, int* chunk) {
+        // parts of at least 256 keys (four rounds of a CTA), as long as SMs are idle
+        const long long want = 2LL * num_sms / ctas, most = n / 256;
+        const long long p = want < most ? want : most;
+        *parts = p > 1 ? (int)p : 1;
+        *chunk = (int)((n + *parts - 1) / *parts + 63) / 64 * 64;
+        if (*chunk == 0) *chunk = 64;
+    };
+    if (attn_rows_takes(a, rows)) {
+        const bool group = a.B > 1 && a.shared.n > 0 && attn_rows_takes(a, a.B * rows) && keys > 512;
+        if (group) {
+            a.walk = 0;
+            cut(a.shared.n, (long long)a.Hkv, &a.parts_shared, &a.chunk_shared);
+            cut(a.own.n, ctas, &a.parts_own, &a.chunk_own);
+        } else {
+            cut(keys, ctas, &a.parts_own, &a.chunk_own);
+        }
+    }
+    const int parts = a.parts_own + a.parts_shared;
+    if (parts == 1) return 0;
+    return (size_t)parts * a.B * a.T * a.Hq * (a.d + 1) * 4;
+}
+
+template <int DIM, typename T>
+static void launch_simple(const AttnArgs& a, cudaStream_t s) {
+    const dim3 grid((a.T * a.Gq + kAtRows - 1) / kAtRows, a.Hkv, a.B);
+    attn_kernel<DIM, T><<<grid, 256, 0, s>>>(a);
+}
+
+cudaError_t launch_attn(const AttnArgs& a, int num_sms, int* launches, cudaStream_t s) {
+    (void)num_sms;
+    *launches = 1;
+    if (attn_rows_takes(a, a.T * a.Gq)) {
+        cudaError_t e = launch_attn_rows(a, s);
+        if (e != cudaSuccess || !a.part_o) return e;
+        *launches = 2;
+        const unsigned grid = (unsigned)(((size_t)a.B * a.T * a.Hq + 3) / 4);
+        if (a.d == 128) attn_join_kernel<128, __nv_bfloat16><<<grid, 128, 0, s>>>(a);
+        else attn_join_kernel<64, __nv_bfloat16><<<grid, 128, 0, s>>>(a);
+        return cudaGetLastError();
+    }
+    if (a.dtype == 1) a.d == 128 ? launch_simple<128, __nv_bfloat16>(a, s) : launch_simple<64, __nv_bfloat16>(a, s);
+    else a.d == 128 ? launch_simple<128, float>(a, s) : launch_simple<64, float>(a, s);
     return cudaGetLastError();
 }
 

@@ -31,8 +31,45 @@ struct AttnArgs {
     int causal;            // query t reads own keys s <= len - T + t (else s < len)
     int B, T, Hq, Hkv, Gq, d, dtype;
     float scale_log2;      // scale * log2(e)
+    // How the work is cut (plan_attn).  A part is what one CTA makes of a row: its sum over a
+    // range of keys.  With one part the CTA writes y; else it leaves the normalised sum and
+    // its log2-sum-exp in the workspace and attn_join_kernel puts the parts together.
+    int walk;              // 1: a sequence's rows read the shared keys too, before their own;
+                           // 0: the shared keys are read by all sequences' rows as one group
+    int parts_shared, parts_own;       // parts of a row from each kind of CTA (walk: all are own)
+    int chunk_shared, chunk_own;       // keys per part
+    float* part_o;         // [parts][B T Hq][d]
+    float* part_l;         // [parts][B T Hq]
 };
 
-cudaError_t launch_attn(const AttnArgs& a, cudaStream_t s);
+// Chooses how the keys are cut (every field after scale_log2 but the pointers) and returns the
+// bytes of workspace that needs.
+size_t plan_attn(AttnArgs& a, int num_sms);
+cudaError_t launch_attn(const AttnArgs& a, int num_sms, int* launches, cudaStream_t s);
+cudaError_t launch_attn_rows(const AttnArgs& a, cudaStream_t s);       // bf16, few rows per group (attn_rows.cu)
+bool attn_rows_takes(const AttnArgs& a, int rows);
+
+// Where row r of a group is: its token over the batch, its offset in q (elements), its index in y.
+struct RowAt {
+    int n, t;
+    long long q;
+    size_t o;
+};
+__device__ __forceinline__ RowAt row_at(const AttnArgs& a, int n0, int g, int r) {
+    RowAt x;
+    x.n = n0 + r / a.Gq;
+    const int h = g * a.Gq + r % a.Gq, b = x.n / a.T;
+    x.t = x.n - b * a.T;
+    x.q = b * a.qb + x.t * a.qs + h * a.qh;
+    x.o = (size_t)x.n * a.Hq + h;
+    return x;
+}
+__device__ __forceinline__ int own_length(const AttnArgs& a, int b) {
+    return a.own_len ? min(max(a.own_len[b], 0), a.own.n) : a.own.n;
+}
+// own keys that query t reads, of a sequence that has len
+__device__ __forceinline__ int own_visible(const AttnArgs& a, int len, int t) {
+    return a.causal ? min(len, max(0, len - a.T + t + 1)) : len;
+}
 
 }  // namespace lola

@@ -28,6 +28,8 @@ int check_config(const lola_attn_config* c) {
     if ((double)c->B * c->T * c->Hq >= 2147483648.0)
         return report(LOLA_ERR_UNSUPPORTED, "B * T * Hq = %g is not below 2^31", (double)c->B * c->T * c->Hq);
     if (c->P < 0 || c->L < 0) return report(LOLA_ERR_INVALID_ARG, "negative key count: P=%d L=%d", c->P, c->L);
+    if ((double)c->P + c->L >= 2147000000.0)
+        return report(LOLA_ERR_UNSUPPORTED, "P + L = %g keys", (double)c->P + c->L);
     if (c->d != 64 && c->d != 128) return report(LOLA_ERR_UNSUPPORTED, "d=%d (64 or 128)", c->d);
     if (c->dtype != LOLA_DTYPE_F32 && c->dtype != LOLA_DTYPE_BF16)
         return report(LOLA_ERR_INVALID_ARG, "dtype=%d", c->dtype);
@@ -49,10 +51,32 @@ int check_config(const lola_attn_config* c) {
     return LOLA_OK;
 }
 
+lola::AttnArgs make_args(const lola_attn_config* c, int causal) {
+    lola::AttnArgs a{};
+    a.qb = c->q_stride[0]; a.qs = c->q_stride[1]; a.qh = c->q_stride[2];
+    a.shared = {nullptr, nullptr, 0, c->kp_stride[0], c->kp_stride[1], 0, c->vp_stride[0], c->vp_stride[1], c->P};
+    a.own = {nullptr, nullptr, c->k_stride[0], c->k_stride[1], c->k_stride[2], c->v_stride[0], c->v_stride[1],
+             c->v_stride[2], c->L};
+    a.causal = causal;
+    a.B = c->B; a.T = c->T; a.Hq = c->Hq; a.Hkv = c->Hkv; a.Gq = c->Hq / c->Hkv; a.d = c->d; a.dtype = c->dtype;
+    a.scale_log2 = c->scale * 1.4426950408889634f;
+    return a;
+}
+
+// SMs of the current device; without one (size queries on a host without a GPU) those of a B200.
+int sm_count() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return 148;
+    }
+    return sms;
+}
+
 int run(const lola_attn_config* c, int causal, const void* q, const void* kp, const void* vp, const void* k,
         const void* v, const int* len, void* y, float* lse, void* workspace, size_t bytes, void* stream) {
-    size_t need = 0;
-    if (int rc = lola_attn_workspace(c, &need)) return rc;
+    if (int rc = check_config(c)) return rc;
     if (!q || !y || (c->P > 0 && (!kp || !vp)) || (c->L > 0 && (!k || !v)))
         return report(LOLA_ERR_INVALID_ARG, "null argument");
     if (misaligned(q) || misaligned(y) || (c->P > 0 && (misaligned(kp) || misaligned(vp))) ||
@@ -60,23 +84,26 @@ int run(const lola_attn_config* c, int causal, const void* q, const void* kp, co
         return report(LOLA_ERR_INVALID_ARG, "q, k, v and y must be 16-byte aligned");
     if (((uintptr_t)len | (uintptr_t)lse) & 3)
         return report(LOLA_ERR_INVALID_ARG, "lengths and lse must be 4-byte aligned");
+    const int sms = sm_count();
+    lola::AttnArgs a = make_args(c, causal);
+    const size_t need = lola::plan_attn(a, sms);
     if (need && (!workspace || ((uintptr_t)workspace & 255)))
         return report(LOLA_ERR_INVALID_ARG, "workspace must be a 256-byte aligned pointer");
     if (bytes < need) return report(LOLA_ERR_BUF_TOO_SMALL, "workspace has %zu bytes, needs %zu", bytes, need);
-    lola::AttnArgs a{};
-    a.q = q; a.qb = c->q_stride[0]; a.qs = c->q_stride[1]; a.qh = c->q_stride[2];
+    a.q = q;
     a.y = y;
     a.lse = lse;
-    a.shared = {kp, vp, 0, c->kp_stride[0], c->kp_stride[1], 0, c->vp_stride[0], c->vp_stride[1], c->P};
-    a.own = {k, v, c->k_stride[0], c->k_stride[1], c->k_stride[2], c->v_stride[0], c->v_stride[1], c->v_stride[2],
-             c->L};
+    a.shared.k = kp; a.shared.v = vp;
+    a.own.k = k; a.own.v = v;
     a.own_len = len;
-    a.causal = causal;
-    a.B = c->B; a.T = c->T; a.Hq = c->Hq; a.Hkv = c->Hkv; a.Gq = c->Hq / c->Hkv; a.d = c->d; a.dtype = c->dtype;
-    a.scale_log2 = c->scale * 1.4426950408889634f;
-    const cudaError_t e = lola::launch_attn(a, (cudaStream_t)stream);
+    if (need) {
+        a.part_o = (float*)workspace;
+        a.part_l = a.part_o + need / ((a.d + 1) * 4) * a.d;
+    }
+    int launches = 0;
+    const cudaError_t e = lola::launch_attn(a, sms, &launches, (cudaStream_t)stream);
     if (e != cudaSuccess) return report(LOLA_ERR_CUDA, "attention kernel: %s", cudaGetErrorString(e));
-    lola::count_launches(1);
+    lola::count_launches(launches);
     return LOLA_OK;
 }
 
@@ -87,7 +114,9 @@ extern "C" {
 int lola_attn_workspace(const lola_attn_config* cfg, size_t* bytes) {
     if (int rc = check_config(cfg)) return rc;
     if (!bytes) return report(LOLA_ERR_INVALID_ARG, "null bytes pointer");
-    *bytes = 0;
+    // (the causal limit does not enter the plan: one size serves both calls)
+    lola::AttnArgs a = make_args(cfg, 0);
+    *bytes = lola::plan_attn(a, sm_count());
     return LOLA_OK;
 }
 
