@@ -269,8 +269,10 @@ int lola_state_fork(lola_state* dst, const lola_state* src, const int* parents, 
  * layers are hybrid.  Row (b, t, h) of the queries reads kv head h / (Hq / Hkv):
  *   y[b][t][h] = sum_i p_i v_i,   p = softmax over its keys i of scale q . k_i,
  *   lse[b][t][h] = log sum_i exp(scale q . k_i)   (natural log).
- * A row that reads no key gets y = 0 and lse = -infinity.  Keys that a row does
- * not read never reach its result, whatever they hold (NaN and infinities too).
+ * A row that reads no key gets y = 0 and lse = -infinity.  Keys and values behind
+ * a sequence's length never reach a result, whatever they hold (NaN and
+ * infinities too).  Values of its later tokens must be finite: a query that
+ * does not read them multiplies them by 0.
  * y is in dtype (its next use is a projection in that type), lse float32.
  * Precision: bf16 inputs multiply on the tensor cores with f32 accumulation;
  * f32 inputs, the softmax statistics and the sums are f32.
@@ -317,6 +319,12 @@ int lola_cross_attention(const lola_attn_config* cfg, const void* q, const void*
 int lola_prefix_attention(const lola_attn_config* cfg, const void* q, const void* k_prefix, const void* v_prefix,
                           const void* k, const void* v, const int* own_len, void* y, float* lse, void* workspace,
                           size_t bytes, void* stream);
+
+/* Sync point for the two calls above: waits for `stream` and returns
+ * LOLA_ERR_TIMEOUT if a bounded device-side wait of any attention call on the
+ * current device gave up since the last check (their results are not valid),
+ * LOLA_ERR_CUDA if the stream reports an error, LOLA_OK otherwise. */
+int lola_attn_check(void* stream);
 
 /* Fill *out with device views of the state (no copy, no synchronisation). */
 int lola_state_export(const lola_state* st, lola_state_view* out);

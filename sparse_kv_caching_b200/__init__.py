@@ -29,7 +29,7 @@ EXPORTS = ("lola_state_bytes", "lola_state_init", "lola_state_reset", "lola_stat
            "lola_profile_read", "lola_launch_count", "lola_prefill_once_noalloc", "lola_selftest_umma",
            "lola_set_read_options", "lola_sre_map", "lola_set_scorer", "lola_state_check",
            "lola_set_batch", "lola_state_fork", "lola_attn_workspace", "lola_cross_attention",
-           "lola_prefix_attention",
+           "lola_prefix_attention", "lola_attn_check",
            "lola_last_error_string")
 KERNEL_CLASSES = ("phi", "scan", "output", "finalize", "decode", "sre_map", "scores")
 READ_HIDE_STATE, READ_HIDE_SPARSE = 1, 2
@@ -95,6 +95,7 @@ def lib() -> ctypes.CDLL:
     L.lola_attn_workspace.argtypes = [POINTER(LolaAttnConfig), POINTER(c_size_t)]
     L.lola_cross_attention.argtypes = [POINTER(LolaAttnConfig), vp, vp, vp, vp, vp, vp, vp, c_size_t, vp]
     L.lola_prefix_attention.argtypes = [POINTER(LolaAttnConfig), vp, vp, vp, vp, vp, vp, vp, vp, vp, c_size_t, vp]
+    L.lola_attn_check.argtypes = [vp]
     L.lola_launch_count.argtypes = []
     L.lola_launch_count.restype = c_longlong
     L.lola_last_error_string.argtypes = []
@@ -230,6 +231,12 @@ def attention_workspace(q, k, k_prefix=None) -> int:
     n = c_size_t()
     _check(lib().lola_attn_workspace(byref(c), byref(n)))
     return n.value
+
+
+def attention_check(stream=None) -> None:
+    """Sync point: wait for the stream and raise LolaError (LOLA_ERR_TIMEOUT) if a bounded device-side
+    wait of an attention call on the current device gave up since the last check."""
+    _check(lib().lola_attn_check(_stream(stream)))
 
 
 def cross_attention(q, k, v, kv_len=None, scale=None, y=None, lse=None, workspace=None, stream=None):

@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
     const size_t rows = (size_t)a.B * a.T * a.Hq, row = (size_t)blockIdx.x * 4 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     if (row >= rows) return;
-    const int np = a.parts_own + (a.walk ? 0 : a.parts_shared);
+    const int np = a.parts_own + a.parts_shared;
     float m = -INFINITY;
     for (int p = lane; p < np; p += 32) m = fmaxf(m, a.part_l[p * rows + row]);
     m = warp_max(m);
@@ -135,27 +135,57 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
 
 size_t plan_attn(AttnArgs& a, int num_sms) {
     a.walk = 1;
-    a.parts_shared = 0;
-    a.parts_own = 1;
-    a.chunk_shared = a.chunk_own = 0;
-    const int rows = a.T * a.Gq;
-    const long long keys = (long long)a.shared.n + a.own.n, ctas = (long long)a.B * a.Hkv;
-    auto cut = [&](long long n, long long ctas, int* parts, int* chunk) {
-        // parts of at least 256 keys (four rounds of a CTA), as long as SMs are idle
-        const long long want = 2LL * num_sms / ctas, most = n / 256;
-        const long long p = want < most ? want : most;
-        *parts = p > 1 ? (int)p : 1;
-        *chunk = (int)((n + *parts - 1) / *parts + 63) / 64 * 64;
+    a.by_shared = a.by_own = AttnBy::none;
+    a.parts_shared = a.parts_own = a.chunk_shared = a.chunk_own = 0;
+    const int rows = a.T * a.Gq, P = a.shared.n, L = a.own.n;
+    const long long groups = (long long)a.B * a.Hkv, all_rows = (long long)a.B * rows;
+    auto tiles = [](long long n, long long of) { return (n + of - 1) / of; };
+    // Few rows: two CTAs per SM, parts of at least 256 keys (four rounds of a CTA).  Tiles: one
+    // CTA per SM, parts of at least four key tiles.
+    auto cut_rows = [&](long long n, long long ctas, int* parts, int* chunk) {
+        long long k = 2LL * num_sms / ctas;
+        if (k > n / 256) k = n / 256;
+        if (k < 1) k = 1;
+        *chunk = (int)(tiles(tiles(n, k), 64) * 64);
         if (*chunk == 0) *chunk = 64;
+        *parts = n > 0 ? (int)tiles(n, *chunk) : 1;
     };
-    if (attn_rows_takes(a, rows)) {
-        const bool group = a.B > 1 && a.shared.n > 0 && attn_rows_takes(a, a.B * rows) && keys > 512;
-        if (group) {
-            a.walk = 0;
-            cut(a.shared.n, (long long)a.Hkv, &a.parts_shared, &a.chunk_shared);
-            cut(a.own.n, ctas, &a.parts_own, &a.chunk_own);
+    auto cut_tiles = [&](long long n, long long ctas, int* parts, int* chunk) {
+        long long k = num_sms / ctas;
+        if (k > n / 4) k = n / 4;
+        if (k < 1) k = 1;
+        const long long c = tiles(n, k) > 0 ? tiles(n, k) : 1;
+        *chunk = (int)(c * 128);
+        *parts = n > 0 ? (int)tiles(n, c) : 1;
+    };
+    if (a.dtype != 1) {
+        a.by_own = AttnBy::simple;
+        a.parts_own = 1;
+        return 0;
+    }
+    // The shared keys once for the whole batch, or again for each sequence (from L2)?  Apart,
+    // when that saves row tiles; together, a row needs no join.
+    if (a.B > 1 && P > 512) {
+        const int of = all_rows <= kRowsMax ? kRowsMax : 128;
+        a.walk = a.B * tiles(rows, of) < 2 * tiles(all_rows, of);
+    }
+    if (!a.walk) {
+        if (all_rows <= kRowsMax) {
+            a.by_shared = AttnBy::rows;
+            cut_rows(P, a.Hkv, &a.parts_shared, &a.chunk_shared);
         } else {
-            cut(keys, ctas, &a.parts_own, &a.chunk_own);
+            a.by_shared = AttnBy::tiles;
+            cut_tiles(tiles(P, 128), tiles(all_rows, 256) * a.Hkv, &a.parts_shared, &a.chunk_shared);
+        }
+    }
+    if (a.walk || L > 0) {
+        const long long n = (a.walk ? P : 0) + (long long)L;
+        if (rows <= kRowsMax) {
+            a.by_own = AttnBy::rows;
+            cut_rows(n, groups, &a.parts_own, &a.chunk_own);
+        } else {
+            a.by_own = AttnBy::tiles;
+            cut_tiles((a.walk ? tiles(P, 128) : 0) + tiles(L, 128), tiles(rows, 256) * groups, &a.parts_own, &a.chunk_own);
         }
     }
     const int parts = a.parts_own + a.parts_shared;
@@ -170,20 +200,28 @@ static void launch_simple(const AttnArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_attn(const AttnArgs& a, int num_sms, int* launches, cudaStream_t s) {
-    (void)num_sms;
-    *launches = 1;
-    if (attn_rows_takes(a, a.T * a.Gq)) {
-        cudaError_t e = launch_attn_rows(a, s);
-        if (e != cudaSuccess || !a.part_o) return e;
-        *launches = 2;
+    *launches = 0;
+    if (a.by_own == AttnBy::simple) {
+        a.d == 128 ? launch_simple<128, float>(a, s) : launch_simple<64, float>(a, s);
+        ++*launches;
+        return cudaGetLastError();
+    }
+    cudaError_t e = cudaSuccess;
+    auto run = [&](cudaError_t x) {
+        e = x;
+        ++*launches;
+        return x == cudaSuccess;
+    };
+    if (a.by_shared == AttnBy::tiles && !run(launch_attn_tc(a, 1, num_sms, s))) return e;
+    if (a.by_own == AttnBy::tiles && !run(launch_attn_tc(a, 0, num_sms, s))) return e;
+    if ((a.by_shared == AttnBy::rows || a.by_own == AttnBy::rows) && !run(launch_attn_rows(a, s))) return e;
+    if (a.part_o) {
         const unsigned grid = (unsigned)(((size_t)a.B * a.T * a.Hq + 3) / 4);
         if (a.d == 128) attn_join_kernel<128, __nv_bfloat16><<<grid, 128, 0, s>>>(a);
         else attn_join_kernel<64, __nv_bfloat16><<<grid, 128, 0, s>>>(a);
-        return cudaGetLastError();
+        run(cudaGetLastError());
     }
-    if (a.dtype == 1) a.d == 128 ? launch_simple<128, __nv_bfloat16>(a, s) : launch_simple<64, __nv_bfloat16>(a, s);
-    else a.d == 128 ? launch_simple<128, float>(a, s) : launch_simple<64, float>(a, s);
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace lola

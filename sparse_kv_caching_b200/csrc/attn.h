@@ -20,6 +20,8 @@ struct KeySeg {            // one segment of keys; strides in elements
     int n;                               // keys (per sequence)
 };
 
+enum class AttnBy { none, rows, tiles, simple };
+
 struct AttnArgs {
     const void* q;
     long long qb, qs, qh;
@@ -36,7 +38,8 @@ struct AttnArgs {
     // its log2-sum-exp in the workspace and attn_join_kernel puts the parts together.
     int walk;              // 1: a sequence's rows read the shared keys too, before their own;
                            // 0: the shared keys are read by all sequences' rows as one group
-    int parts_shared, parts_own;       // parts of a row from each kind of CTA (walk: all are own)
+    AttnBy by_shared, by_own;          // the kernels of the group over all sequences and of each sequence
+    int parts_shared, parts_own;       // parts of a row from each (0: that kernel has nothing to do)
     int chunk_shared, chunk_own;       // keys per part
     float* part_o;         // [parts][B T Hq][d]
     float* part_l;         // [parts][B T Hq]
@@ -46,8 +49,12 @@ struct AttnArgs {
 // bytes of workspace that needs.
 size_t plan_attn(AttnArgs& a, int num_sms);
 cudaError_t launch_attn(const AttnArgs& a, int num_sms, int* launches, cudaStream_t s);
-cudaError_t launch_attn_rows(const AttnArgs& a, cudaStream_t s);       // bf16, few rows per group (attn_rows.cu)
-bool attn_rows_takes(const AttnArgs& a, int rows);
+// bf16, up to kRowsMax rows per group (attn_rows.cu); the parts of both kinds that are its own
+constexpr int kRowsMax = 32;
+cudaError_t launch_attn_rows(const AttnArgs& a, cudaStream_t s);
+// bf16, any number of rows, 128 keys at a time (attn_tc.cu); packed: the shared keys' group
+cudaError_t launch_attn_tc(const AttnArgs& a, int packed, int num_sms, cudaStream_t s);
+cudaError_t attn_error_word(int* word, cudaStream_t s);
 
 // Where row r of a group is: its token over the batch, its offset in q (elements), its index in y.
 struct RowAt {

@@ -74,6 +74,19 @@ int sm_count() {
     return sms;
 }
 
+// One encoder output for all sequences, all of it read: the keys are shared.
+bool keys_shared(const lola_attn_config* c) {
+    return c->P == 0 && c->B > 1 && c->L > 0 && c->k_stride[0] == 0 && c->v_stride[0] == 0;
+}
+lola_attn_config as_shared(const lola_attn_config& c) {
+    lola_attn_config x = c;
+    x.P = c.L;
+    x.L = 0;
+    x.kp_stride[0] = c.k_stride[1]; x.kp_stride[1] = c.k_stride[2];
+    x.vp_stride[0] = c.v_stride[1]; x.vp_stride[1] = c.v_stride[2];
+    return x;
+}
+
 int run(const lola_attn_config* c, int causal, const void* q, const void* kp, const void* vp, const void* k,
         const void* v, const int* len, void* y, float* lse, void* workspace, size_t bytes, void* stream) {
     if (int rc = check_config(c)) return rc;
@@ -116,13 +129,25 @@ int lola_attn_workspace(const lola_attn_config* cfg, size_t* bytes) {
     if (!bytes) return report(LOLA_ERR_INVALID_ARG, "null bytes pointer");
     // (the causal limit does not enter the plan: one size serves both calls)
     lola::AttnArgs a = make_args(cfg, 0);
-    *bytes = lola::plan_attn(a, sm_count());
+    const int sms = sm_count();
+    *bytes = lola::plan_attn(a, sms);
+    if (keys_shared(cfg)) {
+        const lola_attn_config x = as_shared(*cfg);
+        a = make_args(&x, 0);
+        const size_t n = lola::plan_attn(a, sms);
+        if (n > *bytes) *bytes = n;
+    }
     return LOLA_OK;
 }
 
 int lola_cross_attention(const lola_attn_config* cfg, const void* q, const void* k, const void* v, const int* kv_len,
                          void* y, float* lse, void* workspace, size_t bytes, void* stream) {
     if (cfg && cfg->P != 0) return report(LOLA_ERR_INVALID_ARG, "P=%d: cross attention has no shared prefix", cfg->P);
+    if (int rc = check_config(cfg)) return rc;
+    if (!kv_len && keys_shared(cfg)) {
+        const lola_attn_config x = as_shared(*cfg);
+        return run(&x, 0, q, k, v, nullptr, nullptr, nullptr, y, lse, workspace, bytes, stream);
+    }
     return run(cfg, 0, q, nullptr, nullptr, k, v, kv_len, y, lse, workspace, bytes, stream);
 }
 
@@ -130,6 +155,16 @@ int lola_prefix_attention(const lola_attn_config* cfg, const void* q, const void
                           const void* k, const void* v, const int* own_len, void* y, float* lse, void* workspace,
                           size_t bytes, void* stream) {
     return run(cfg, 1, q, k_prefix, v_prefix, k, v, own_len, y, lse, workspace, bytes, stream);
+}
+
+int lola_attn_check(void* stream) {
+    int word = 0;
+    const cudaError_t e = lola::attn_error_word(&word, (cudaStream_t)stream);
+    if (e != cudaSuccess) return report(LOLA_ERR_CUDA, "reading the attention error word: %s", cudaGetErrorString(e));
+    if (word)
+        return report(LOLA_ERR_TIMEOUT, "a bounded device-side wait of an attention call gave up since the last check; "
+                      "the results of the calls since then are not valid");
+    return LOLA_OK;
 }
 
 }  // extern "C"

@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kRwWarps * 32) attn_rows_kernel(const __grid_c
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
     // ---- which rows, which keys ----
-    const int n_sh = a.walk ? 0 : a.parts_shared * a.Hkv;             // CTAs of the shared group
+    const int n_sh = a.by_shared == AttnBy::rows ? a.parts_shared * a.Hkv : 0;      // CTAs of the shared group
     int g, b = 0, part, lo, hi, n0, R, np0;     // np0: keys of the walk that are shared ones
     if ((int)blockIdx.x < n_sh) {
         part = blockIdx.x % a.parts_shared;
@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kRwWarps * 32) attn_rows_kernel(const __grid_c
         np0 = a.walk ? a.shared.n : 0;
         lo = part * a.chunk_own;
         hi = (int)min((long long)np0 + own_length(a, b), (long long)lo + a.chunk_own);
-        part += a.walk ? 0 : a.parts_shared;
+        part += a.parts_shared;
     }
     const int len = (int)blockIdx.x < n_sh ? 0 : own_length(a, b);
     const bf16* ksh = (const bf16*)a.shared.k + (long long)g * a.shared.kh;
@@ -288,16 +288,14 @@ static cudaError_t launch_rows_t(const AttnArgs& a, cudaStream_t s) {
     using Sh = RowsShape<DIM, MT>;
     cudaError_t e = cudaFuncSetAttribute(attn_rows_kernel<DIM, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::BYTES);
     if (e != cudaSuccess) return e;
-    const unsigned grid = (a.walk ? 0 : a.parts_shared * a.Hkv) + a.parts_own * a.Hkv * a.B;
+    const unsigned grid = (a.by_shared == AttnBy::rows ? a.parts_shared * a.Hkv : 0) +
+                          (a.by_own == AttnBy::rows ? a.parts_own * a.Hkv * a.B : 0);
     attn_rows_kernel<DIM, MT><<<grid, kRwWarps * 32, Sh::BYTES, s>>>(a);
     return cudaGetLastError();
 }
 
-bool attn_rows_takes(const AttnArgs& a, int rows) { return a.dtype == 1 && rows <= 32; }
-
 cudaError_t launch_attn_rows(const AttnArgs& a, cudaStream_t s) {
-    int rows = a.T * a.Gq;
-    if (!a.walk && a.parts_shared) rows = a.B * a.T * a.Gq;
+    const int rows = (a.by_shared == AttnBy::rows ? a.B : 1) * a.T * a.Gq;
     if (a.d == 128) return rows <= 16 ? launch_rows_t<128, 1>(a, s) : launch_rows_t<128, 2>(a, s);
     return rows <= 16 ? launch_rows_t<64, 1>(a, s) : launch_rows_t<64, 2>(a, s);
 }

@@ -1,0 +1,476 @@
+// Exact attention for many rows per kv head (prompts, and the rows of a whole
+// batch against its shared prefix) on the fifth-generation tensor cores, bf16.
+//
+// Mathematics: one pass over tiles of 128 keys with a running reference r of the
+// softmax exponents.  S = Q K^T (tensor cores, f32); P = 2^(c S - r), c =
+// scale log2(e); l += row sums of P in f32; O += P V with P rounded to bf16 (its
+// product's type; half a step, 2^-8 of each weight, averages out over the keys,
+// while f16 weights would need V converted).  r is raised only when a row's
+// maximum passes r + 8, which keeps P below 2^8 and makes rescaling O rare.
+//
+// Bound: the tensor cores (4 d operations per row and key) and, as hard, the
+// exponentials: a 128 x 128 tile costs 1056 cycles of products and 1024 of the
+// special-function unit.  So one CTA per SM works on two 128-row tiles A and B in
+// turn: while the warps of A turn S_A into P_A, the tensor cores run B's
+// products.  Both tiles read the same key tiles, which halves the reads from L2.
+//   warps 0-3 / 4-7  softmax and output of tile A / B; thread r owns row r
+//   warp 8           loads K and V tiles with TMA into a ring (128-byte swizzle)
+//   warp 9           issues the products
+//   warps 10-11      gather the query rows of the next work item
+// Tensor memory: S_A, S_B (128 columns each; P as bf16 pairs over its own S), O_A,
+// O_B.  S_t(j + 1) overwrites P_t(j) right behind O_t += P_t(j) V(j) in the same
+// in-order queue, so S(j + 1) ready also means that O_t may be rescaled.
+// CTAs are persistent: the next item's queries and keys load during the last
+// products and the output of this one.
+// Every wait is bounded; one that gives up raises a flag that ends all others of
+// the CTA, and sets the device's error word.
+#include <cuda.h>
+
+#include "attn.h"
+#include "device_common.cuh"
+#include "umma.cuh"
+
+namespace lola {
+
+__device__ int g_attn_err;
+
+constexpr int kTcRows = 128, kTcKeys = 128, kTcThreads = 384;
+
+struct TcArgs {
+    CUtensorMap map[4];             // shared keys and values, own keys and values
+    AttnArgs a;
+    int packed;                     // 1: items are rows of the whole batch against the shared keys
+    int row_tiles;                  // 256-row tile pairs per group
+    int parts, chunk;               // key tiles per part
+    int part0;                      // first part's index in the workspace
+    int items;
+    int mh[4], mb[4];               // coordinate multipliers of the maps: 0 where one head (sequence) serves all
+};
+
+template <int DIM>
+struct TcShape {
+    static constexpr int QB = kTcRows * DIM * 2, ST = kTcKeys * DIM * 2, NST = DIM == 128 ? 5 : 8;
+    static constexpr int Q = 0, RING = 2 * QB, MBAR = RING + NST * ST;
+    static constexpr int NBAR = 2 * NST + 11;
+    static constexpr int FLAG = MBAR + NBAR * 8, BYTES = FLAG + 16 + 1024;
+    static_assert(BYTES <= 227 * 1024, "shared memory");
+    static constexpr uint32_t TS = 0, TO = 256;       // + 128 per row tile
+    // barriers
+    static constexpr int FULL = 0, FREE = NST, QFULL = 2 * NST, QFREE = QFULL + 2, SFULL = QFREE + 2,
+                         PFULL = SFULL + 2, OFULL = PFULL + 2, DONE = OFULL + 2;
+};
+
+__device__ __forceinline__ bool tc_wait(uint64_t* mbar, uint32_t parity, volatile int* abort) {
+    if (umma::mbar_try_wait(mbar, parity)) return true;
+    const uint64_t t0 = umma::globaltimer_ns();
+    while (!umma::mbar_try_wait(mbar, parity)) {
+        if (*abort) return false;
+        if (umma::globaltimer_ns() - t0 > 4000000000ull) { *abort = 1; return false; }
+    }
+    return true;
+}
+__device__ __forceinline__ float tc_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t tc_pack(float lo, float hi) {
+    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&v);
+}
+__device__ __forceinline__ void tc_tma(void* dst, const CUtensorMap* map, uint64_t* mbar, int key, int h, int b) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2,%3,%4,%5,%6}], [%7];"
+        :: "r"(umma::smem_addr(dst)), "l"(map), "r"(0), "r"(key), "r"(0), "r"(h), "r"(b), "r"(umma::smem_addr(mbar))
+        : "memory");
+}
+__device__ __forceinline__ void tc_expect(uint64_t* mbar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" :: "r"(umma::smem_addr(mbar)), "r"(bytes) : "memory");
+}
+
+// One work item: up to 256 rows of a group against a range of key tiles.
+struct TcItem {
+    int g, b, n0, R, r0, part;      // kv head, sequence, first token, rows of the group, first row, part
+    int nt0, j0, j1, len;           // shared tiles of the walk, this part's tiles, own length
+    bool two;                       // tile B holds rows
+};
+__device__ __forceinline__ TcItem tc_item(const TcArgs& p, int i) {
+    const AttnArgs& a = p.a;
+    TcItem x;
+    const int rt = i % p.row_tiles;
+    i /= p.row_tiles;
+    x.part = i % p.parts;
+    i /= p.parts;
+    x.g = i % a.Hkv;
+    x.b = i / a.Hkv;
+    x.n0 = x.b * a.T;
+    x.R = (p.packed ? a.B : 1) * a.T * a.Gq;
+    x.r0 = rt * 2 * kTcRows;
+    const int last = min(x.R, x.r0 + 2 * kTcRows) - 1;
+    x.two = last >= x.r0 + kTcRows;
+    x.len = p.packed ? 0 : own_length(a, x.b);
+    x.nt0 = p.packed || a.walk ? (a.shared.n + kTcKeys - 1) / kTcKeys : 0;
+    const int vis = p.packed ? 0 : own_visible(a, x.len, last / a.Gq);
+    const int nt = x.nt0 + (vis + kTcKeys - 1) / kTcKeys;
+    x.j0 = min(nt, x.part * p.chunk);
+    x.j1 = min(nt, x.j0 + p.chunk);
+    return x;
+}
+
+template <int DIM>
+__global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_constant__ TcArgs p) {
+    using Sh = TcShape<DIM>;
+    using bf16 = __nv_bfloat16;
+    constexpr int NST = Sh::NST;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (umma::smem_addr(smem_raw) & 1023u)) & 1023u);
+    const AttnArgs& a = p.a;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint8_t* sQ = smem + Sh::Q;
+    uint8_t* ring = smem + Sh::RING;
+    uint64_t* mbar = reinterpret_cast<uint64_t*>(smem + Sh::MBAR);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Sh::FLAG);
+    uint32_t* tptr = reinterpret_cast<uint32_t*>(smem + Sh::FLAG + 8);
+
+    if (warp == 0) umma::tmem_alloc(tptr, 512);
+    if (tid == 0) {
+        for (int i = 0; i < Sh::NBAR; ++i) umma::mbar_init(&mbar[i], 1);
+        for (int t = 0; t < 2; ++t) {
+            umma::mbar_init(&mbar[Sh::QFULL + t], 64);
+            umma::mbar_init(&mbar[Sh::PFULL + t], kTcRows);
+        }
+        *abort_flag = 0;
+        umma::fence_mbar_init();
+    }
+    umma::fence_before_sync();
+    __syncthreads();
+    umma::fence_after_sync();
+    const uint32_t tmem = *tptr;
+    // registers: 256 x 208 + 128 x 88 = the 384 x 168 of the launch
+    if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+
+    if (warp == 8) {
+        // ---- K and V tiles: K(j), V(j), K(j + 1), ... into consecutive ring stages ----
+        if (lane == 0) {
+            unsigned n = 0;                       // tiles loaded so far
+            bool ok = true;
+            for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
+                const TcItem x = tc_item(p, i);
+                for (int jj = 2 * x.j0; jj < 2 * x.j1 && ok; ++jj, ++n) {
+                    const int s = n % NST, j = jj >> 1;
+                    if (n >= NST) ok = tc_wait(&mbar[Sh::FREE + s], (n / NST - 1) & 1, abort_flag);
+                    if (!ok) break;
+                    const bool sh = j < x.nt0;
+                    const int which = (sh ? 0 : 2) + (jj & 1);
+                    tc_expect(&mbar[Sh::FULL + s], Sh::ST);
+                    tc_tma(ring + s * Sh::ST, &p.map[which], &mbar[Sh::FULL + s], (sh ? j : j - x.nt0) * kTcKeys,
+                           x.g * p.mh[which], x.b * p.mb[which]);
+                }
+            }
+            if (!ok)                              // given up: the copies in flight still land in this CTA's memory
+                for (unsigned m = n > NST ? n - NST : 0; m < n; ++m)
+                    (void)umma::mbar_wait(&mbar[Sh::FULL + m % NST], (m / NST) & 1, 1000000000ull);
+        }
+    } else if (warp == 9) {
+        // ---- products ----
+        if (lane == 0) {
+            const uint32_t idS = umma::idesc(umma::kBF16, kTcRows, kTcKeys, false, false);
+            const uint32_t idO = umma::idesc(umma::kBF16, kTcRows, DIM, false, true);
+            const uint64_t dQ = umma::sdesc_sw128(umma::smem_addr(sQ), 16, 1024);
+            const uint64_t dK = umma::sdesc_sw128(umma::smem_addr(ring), 16, 1024);
+            const uint64_t dV = umma::sdesc_sw128(umma::smem_addr(ring), kTcKeys * 128, 1024);
+            // Q and K: a step of 16 dims is 32 bytes inside a 128-byte half row, the next half 128 rows on
+            auto scores = [&](int t, int s) {
+                const uint64_t q = dQ + (uint64_t)(t * (Sh::QB / 16)), k = dK + (uint64_t)(s * (Sh::ST / 16));
+#pragma unroll
+                for (int ks = 0; ks < DIM / 16; ++ks) {
+                    const uint64_t step = (uint64_t)((ks >> 2) * kTcRows * 8 + (ks & 3) * 2);
+                    umma::mma_bf16(tmem + Sh::TS + 128 * t, q + step, k + step, idS, ks > 0);
+                }
+                umma::commit(&mbar[Sh::SFULL + t]);
+            };
+            auto values = [&](int t, int s, bool first) {
+                const uint64_t v = dV + (uint64_t)(s * (Sh::ST / 16));
+#pragma unroll
+                for (int ks = 0; ks < kTcKeys / 16; ++ks)
+                    umma::mma_f16_ts(tmem + Sh::TO + 128 * t, tmem + Sh::TS + 128 * t + 8 * ks, v + (uint64_t)(ks * 128),
+                                     idO, ks > 0 || !first);
+            };
+            unsigned n = 0, np[2] = {0, 0}, nq[2] = {0, 0};
+            bool ok = true;
+            for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
+                const TcItem x = tc_item(p, i);
+                const int nt = x.j1 - x.j0, nr = x.two ? 2 : 1;
+                if (nt == 0) continue;
+                auto full = [&](unsigned m) { return tc_wait(&mbar[Sh::FULL + m % NST], (m / NST) & 1, abort_flag); };
+                ok = full(n);
+                for (int t = 0; t < nr && ok; ++t) {
+                    ok = tc_wait(&mbar[Sh::QFULL + t], nq[t] & 1, abort_flag);
+                    ++nq[t];
+                    if (!ok) break;
+                    umma::fence_after_sync();
+                    scores(t, n % NST);
+                    if (nt == 1) umma::commit(&mbar[Sh::QFREE + t]);
+                }
+                if (!ok) break;
+                umma::commit(&mbar[Sh::FREE + n % NST]);
+                for (int j = 0; j < nt && ok; ++j) {
+                    const unsigned nv = n + 2 * j + 1, nk = nv + 1;
+                    const bool more = j + 1 < nt;
+                    ok = full(nv);
+                    for (int t = 0; t < nr && ok; ++t) {
+                        ok = tc_wait(&mbar[Sh::PFULL + t], np[t] & 1, abort_flag);
+                        ++np[t];
+                        if (!ok) break;
+                        umma::fence_after_sync();
+                        values(t, nv % NST, j == 0);
+                        if (!more) { umma::commit(&mbar[Sh::OFULL + t]); continue; }
+                        if (t == 0) ok = full(nk);
+                        if (!ok) break;
+                        scores(t, nk % NST);
+                        if (j + 2 == nt) umma::commit(&mbar[Sh::QFREE + t]);
+                    }
+                    if (!ok) break;
+                    umma::commit(&mbar[Sh::FREE + nv % NST]);
+                    if (more) umma::commit(&mbar[Sh::FREE + nk % NST]);
+                }
+                n += 2 * nt;
+            }
+            umma::commit(&mbar[Sh::DONE]);        // nothing may be in flight when tensor memory is given back
+            if (!umma::mbar_wait(&mbar[Sh::DONE], 0, 4000000000ull)) *abort_flag = 1;
+        }
+    } else if (warp >= 10) {
+        // ---- queries: 128-byte swizzled, block kb holds dims 64 kb .. 64 kb + 63 of every row ----
+        constexpr int NC = DIM / 8;
+        const int w = tid - 320;
+        unsigned nq[2] = {0, 0};
+        bool ok = true;
+        for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
+            const TcItem x = tc_item(p, i);
+            if (x.j0 == x.j1) continue;
+            for (int t = 0; t < (x.two ? 2 : 1) && ok; ++t) {
+                if (nq[t]) ok = tc_wait(&mbar[Sh::QFREE + t], (nq[t] - 1) & 1, abort_flag);
+                ++nq[t];
+                if (!ok) break;
+                for (int idx = w; idx < kTcRows * NC; idx += 64) {
+                    const int r = idx / NC, c = idx % NC, R = x.r0 + t * kTcRows + r;
+                    const bool in = R < x.R;
+                    const RowAt y = row_at(a, x.n0, x.g, in ? R : 0);
+                    umma::cp_async16_zfill(sQ + t * Sh::QB + (c >> 3) * (kTcRows * 128) + umma::sw128_off(r, c & 7),
+                                           (const bf16*)a.q + y.q + 8 * c, in);
+                }
+                umma::cp_async_commit();
+            }
+            if (!ok) break;
+            if (x.two) {
+                umma::cp_async_wait<1>();
+                umma::fence_async_smem();
+                umma::mbar_arrive(&mbar[Sh::QFULL]);
+            }
+            umma::cp_async_wait<0>();
+            umma::fence_async_smem();
+            umma::mbar_arrive(&mbar[Sh::QFULL + (x.two ? 1 : 0)]);
+        }
+        umma::cp_async_wait<0>();
+    } else {
+        // ---- softmax and output of row tile t ----
+        const int t = warp >> 2, r = tid & (kTcRows - 1);
+        const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t tS = tmem + lane_off + Sh::TS + 128 * t, tO = tmem + lane_off + Sh::TO + 128 * t;
+        const float c2 = a.scale_log2;
+        unsigned n = 0, ns = 0, no = 0;           // ring position; tiles and items of this row tile
+        bool dead = false;
+        for (int i = blockIdx.x; i < p.items && !dead; i += gridDim.x) {
+            const TcItem x = tc_item(p, i);
+            if (t == 1 && !x.two) { n += 2 * (x.j1 - x.j0); continue; }
+            const int R = x.r0 + t * kTcRows + r;
+            const bool row_ok = R < x.R;
+            const RowAt at = row_at(a, x.n0, x.g, row_ok ? R : 0);
+            const int vis = row_ok ? own_visible(a, x.len, at.t) : 0, vis0 = row_ok ? a.shared.n : 0;
+            float m = -INFINITY, l = 0.f;
+            for (int j = x.j0; j < x.j1; ++j, ++ns) {
+                bool ok = tc_wait(&mbar[Sh::SFULL + t], ns & 1, abort_flag);
+                if (!__all_sync(0xffffffffu, ok)) { dead = true; break; }
+                umma::fence_after_sync();
+                float s[kTcKeys];
+#pragma unroll
+                for (int c = 0; c < kTcKeys; c += 16) umma::tmem_ld16(tS + c, *reinterpret_cast<float(*)[16]>(s + c));
+                umma::tmem_wait_ld();
+                const bool sh = j < x.nt0;
+                const int k0 = (sh ? j : j - x.nt0) * kTcKeys, lim = (sh ? vis0 : vis) - k0;
+                if (!__all_sync(0xffffffffu, lim >= kTcKeys)) {
+#pragma unroll
+                    for (int u = 0; u < kTcKeys; ++u) s[u] = u < lim ? s[u] : -INFINITY;
+                }
+                float mx = fmaxf(s[0], s[1]);
+#pragma unroll
+                for (int u = 2; u < kTcKeys; u += 2) mx = fmaxf(mx, fmaxf(s[u], s[u + 1]));
+                mx *= c2;
+                float f = 1.f;
+                bool raise = false;
+                if (m == -INFINITY) m = mx;       // nothing read yet
+                else if (mx > m + 8.f) { f = tc_ex2(m - mx); m = mx; raise = true; }
+                const float ref = m == -INFINITY ? 0.f : m;
+                if (__any_sync(0xffffffffu, raise)) {
+                    // every product before S(j) is complete: O is free
+                    l *= f;
+#pragma unroll
+                    for (int c = 0; c < DIM; c += 16) {
+                        float o[16];
+                        umma::tmem_ld16(tO + c, o);
+                        umma::tmem_wait_ld();
+#pragma unroll
+                        for (int u = 0; u < 16; ++u) o[u] *= f;
+                        umma::tmem_st16(tO + c, o);
+                    }
+                }
+                float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+                for (int c = 0; c < kTcKeys; c += 32) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int u = 0; u < 16; ++u) {
+                        const float e0 = tc_ex2(fmaf(s[c + 2 * u], c2, -ref)), e1 = tc_ex2(fmaf(s[c + 2 * u + 1], c2, -ref));
+                        sum0 += e0;
+                        sum1 += e1;
+                        w[u] = tc_pack(e0, e1);
+                    }
+                    umma::tmem_st16(tS + c / 2, *reinterpret_cast<const float(*)[16]>(w));
+                }
+                l += sum0 + sum1;
+                if (t == 0 && !sh && x.len < a.own.n && k0 + kTcKeys > x.len) {
+                    // rows of V behind the sequence's length may hold anything: 0 x NaN is not 0
+                    const unsigned nv = n + 2 * (j - x.j0) + 1;
+                    ok = tc_wait(&mbar[Sh::FULL + nv % NST], (nv / NST) & 1, abort_flag);
+                    if (!__all_sync(0xffffffffu, ok)) { dead = true; break; }
+                    if (r >= x.len - k0) {
+#pragma unroll
+                        for (int c = 0; c < DIM / 8; ++c)
+                            *reinterpret_cast<uint4*>(ring + (nv % NST) * Sh::ST + (c >> 3) * (kTcKeys * 128) + r * 128 +
+                                                      (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    umma::fence_async_smem();
+                }
+                umma::tmem_wait_st();
+                umma::fence_before_sync();
+                umma::mbar_arrive(&mbar[Sh::PFULL + t]);
+            }
+            if (dead) break;
+            n += 2 * (x.j1 - x.j0);
+            const bool any = x.j1 > x.j0;
+            if (any) {
+                const bool ok = tc_wait(&mbar[Sh::OFULL + t], no & 1, abort_flag);
+                ++no;
+                if (!__all_sync(0xffffffffu, ok)) { dead = true; break; }
+                umma::fence_after_sync();
+            }
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const float l2 = l == 0.f ? -INFINITY : m + log2f(l);
+            const size_t rows_all = (size_t)a.B * a.T * a.Hq, po = (size_t)(p.part0 + x.part) * rows_all + at.o;
+#pragma unroll
+            for (int c = 0; c < DIM; c += 32) {
+                float o[32];
+                if (any) {
+                    umma::tmem_ld16(tO + c, *reinterpret_cast<float(*)[16]>(o));
+                    umma::tmem_ld16(tO + c + 16, *reinterpret_cast<float(*)[16]>(o + 16));
+                    umma::tmem_wait_ld();
+                }
+#pragma unroll
+                for (int u = 0; u < 32; ++u) o[u] = l == 0.f ? 0.f : o[u] * inv;
+                if (!row_ok) continue;
+                if (a.part_o) {
+#pragma unroll
+                    for (int u = 0; u < 32; u += 4)
+                        *reinterpret_cast<float4*>(a.part_o + po * DIM + c + u) = make_float4(o[u], o[u + 1], o[u + 2], o[u + 3]);
+                } else {
+#pragma unroll
+                    for (int u = 0; u < 32; u += 8)
+                        *reinterpret_cast<uint4*>((bf16*)a.y + at.o * DIM + c + u) =
+                            make_uint4(tc_pack(o[u], o[u + 1]), tc_pack(o[u + 2], o[u + 3]), tc_pack(o[u + 4], o[u + 5]),
+                                       tc_pack(o[u + 6], o[u + 7]));
+                }
+            }
+            if (row_ok) {
+                if (a.part_o) a.part_l[po] = l2;
+                else if (a.lse) a.lse[at.o] = l2 * 0.6931471805599453f;
+            }
+        }
+    }
+    umma::fence_before_sync();
+    __syncthreads();
+    if (tid == 0 && *abort_flag) atomicOr(&g_attn_err, 1);
+    if (warp == 0) umma::tmem_dealloc(tmem, 512);
+}
+
+namespace {
+
+// A tensor of keys or values as [batch][head][half][key][64 dims]: one box of 128 keys lands as
+// [half][128 keys][128 bytes], swizzled.
+bool tc_map(TcArgs& p, int which, const void* base, int d, int n, long long ks, int H, long long kh, int B, long long kb) {
+    typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                               const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const Encode encode = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            return (Encode) nullptr;
+        return (Encode)f;
+    }();
+    if (!encode) return false;
+    p.mh[which] = H > 1 && kh > 0;
+    p.mb[which] = B > 1 && kb > 0;
+    if (!p.mh[which]) { H = 1; kh = 8; }
+    if (!p.mb[which]) { B = 1; kb = 8; }
+    if (n == 1) ks = 8;
+    const cuuint64_t dims[5] = {64, (cuuint64_t)n, (cuuint64_t)(d / 64), (cuuint64_t)H, (cuuint64_t)B};
+    const cuuint64_t strides[4] = {(cuuint64_t)ks * 2, 128, (cuuint64_t)kh * 2, (cuuint64_t)kb * 2};
+    const cuuint32_t box[5] = {64, kTcKeys, (cuuint32_t)(d / 64), 1, 1}, one[5] = {1, 1, 1, 1, 1};
+    return encode(&p.map[which], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DIM>
+cudaError_t launch_tc_t(const TcArgs& p, int num_sms, cudaStream_t s) {
+    using Sh = TcShape<DIM>;
+    cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<DIM>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::BYTES);
+    if (e != cudaSuccess) return e;
+    attn_tc_kernel<DIM><<<p.items < num_sms ? p.items : num_sms, kTcThreads, Sh::BYTES, s>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attn_tc(const AttnArgs& a, int packed, int num_sms, cudaStream_t s) {
+    TcArgs p{};
+    const KeySeg &sh = a.shared, &ow = a.own;
+    if (sh.n > 0 && (packed || a.walk) && (!tc_map(p, 0, sh.k, a.d, sh.n, sh.ks, a.Hkv, sh.kh, 1, 0) ||
+                                           !tc_map(p, 1, sh.v, a.d, sh.n, sh.vs, a.Hkv, sh.vh, 1, 0)))
+        return cudaErrorInvalidValue;
+    if (ow.n > 0 && !packed && (!tc_map(p, 2, ow.k, a.d, ow.n, ow.ks, a.Hkv, ow.kh, a.B, ow.kb) ||
+                                !tc_map(p, 3, ow.v, a.d, ow.n, ow.vs, a.Hkv, ow.vh, a.B, ow.vb)))
+        return cudaErrorInvalidValue;
+    p.a = a;
+    p.packed = packed;
+    const int rows = (packed ? a.B : 1) * a.T * a.Gq;
+    p.row_tiles = (rows + 2 * kTcRows - 1) / (2 * kTcRows);
+    p.parts = packed ? a.parts_shared : a.parts_own;
+    p.chunk = (packed ? a.chunk_shared : a.chunk_own) / kTcKeys;
+    p.part0 = packed ? 0 : a.parts_shared;
+    p.items = p.row_tiles * p.parts * a.Hkv * (packed ? 1 : a.B);
+    return a.d == 128 ? launch_tc_t<128>(p, num_sms, s) : launch_tc_t<64>(p, num_sms, s);
+}
+
+// Reads and clears this device's error word (waits for the stream).
+cudaError_t attn_error_word(int* word, cudaStream_t s) {
+    cudaError_t e = cudaMemcpyFromSymbolAsync(word, g_attn_err, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    static const int zero = 0;
+    if (e == cudaSuccess && *word) e = cudaMemcpyToSymbolAsync(g_attn_err, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
+    return e;
+}
+
+}  // namespace lola

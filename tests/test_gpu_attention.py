@@ -28,6 +28,8 @@ def _cuda():
     if not torch.cuda.is_available():
         pytest.skip("no CUDA device")
     torch.cuda.set_device(0)
+    yield
+    lola.attention_check()
 
 
 def normal(seed, *shape, dtype=F32, factor=1.0):
