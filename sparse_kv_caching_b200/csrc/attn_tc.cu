@@ -147,9 +147,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
     umma::fence_after_sync();
     const uint32_t tmem = *tptr;
     // registers: 256 x 208 + 128 x 88 = the 384 x 168 of the launch
-    if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-
+    if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 8) {
         // ---- K and V tiles: K(j), V(j), K(j + 1), ... into consecutive ring stages ----
         if (lane == 0) {
@@ -240,7 +239,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             umma::commit(&mbar[Sh::DONE]);        // nothing may be in flight when tensor memory is given back
             if (!umma::mbar_wait(&mbar[Sh::DONE], 0, 4000000000ull)) *abort_flag = 1;
         }
-    } else if (warp >= 10) {
+    } else {
         // ---- queries: 128-byte swizzled, block kb holds dims 64 kb .. 64 kb + 63 of every row ----
         constexpr int NC = DIM / 8;
         const int w = tid - 320;
@@ -273,7 +272,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             umma::mbar_arrive(&mbar[Sh::QFULL + (x.two ? 1 : 0)]);
         }
         umma::cp_async_wait<0>();
+    }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         // ---- softmax and output of row tile t ----
         const int t = warp >> 2, r = tid & (kTcRows - 1);
         const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
