@@ -9,6 +9,7 @@ library is missing or fails to load, every entry point raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from ctypes import POINTER, byref, c_float, c_int, c_longlong, c_size_t, c_void_p, c_char_p
 
@@ -153,10 +154,36 @@ def _stream(stream=None) -> c_void_p:
 
 
 # -- exact attention beside the layer ---------------------------------------------
-def _attn_tensor(x, name, shape, dtype, device, packed=False):
+@functools.lru_cache(maxsize=4096)
+def _attn_plan(qs, ks, ps, q_st, k_st, v_st, kp_st, vp_st, dtype, scale):
+    """(config, bytes of workspace) of a call, from its shapes and strides alone."""
+    if dtype not in _DTYPE_CODE:
+        raise ValueError(f"q: dtype {dtype}, expected one of {list(_DTYPE_CODE)}")
+    if len(qs) != 4 or len(ks) != 4:
+        raise ValueError(f"q and k must have 4 dimensions: shapes {tuple(qs)}, {tuple(ks)}")
+    B, T, Hq, d = qs
+    L, Hkv = ks[1], ks[2]
+    if tuple(ks) != (B, L, Hkv, d):
+        raise ValueError(f"k: shape {tuple(ks)}, expected {(B, L, Hkv, d)}")
+    P = 0
+    if ps is not None:
+        if len(ps) != 3 or tuple(ps[1:]) != (Hkv, d):
+            raise ValueError(f"k_prefix: shape {tuple(ps)}, expected (P, {Hkv}, {d})")
+        P = ps[0]
+    for st, name, n in ((q_st, "q", B * T * Hq), (k_st, "k", L), (v_st, "v", L), (kp_st, "k_prefix", P), (vp_st, "v_prefix", P)):
+        if n and st[-1] != 1:
+            raise ValueError(f"{name}: the head's elements must be contiguous (last stride 1)")
+    c = LolaAttnConfig(B, T, Hq, Hkv, d, _DTYPE_CODE[dtype], P, L, d ** -0.5 if scale is None else scale, q_st[:3],
+                       kp_st[:2] if P else (0, 0), vp_st[:2] if P else (0, 0), k_st[:3], v_st[:3])
+    n = c_size_t()
+    _check(lib().lola_attn_workspace(byref(c), byref(n)))
+    return c, n.value
+
+
+def _attn_same(x, name, shape, dtype, device, packed=False):
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if tuple(x.shape) != tuple(shape):
+    if x.shape != shape:
         raise ValueError(f"{name}: shape {tuple(x.shape)}, expected {tuple(shape)}")
     if x.dtype != dtype:
         raise ValueError(f"{name}: dtype {x.dtype}, expected {dtype}")
@@ -164,59 +191,60 @@ def _attn_tensor(x, name, shape, dtype, device, packed=False):
         raise ValueError(f"{name}: on {x.device}, expected {device}")
     if packed and not x.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if not packed and x.numel() and x.stride(-1) != 1:
-        raise ValueError(f"{name}: the head's elements must be contiguous (last stride 1)")
 
 
-def _attention(entry, q, kp, vp, k, v, lens, lens_name, scale, y, lse, workspace, stream):
-    for x, name in ((q, "q"), (k, "k")):
-        if not isinstance(x, torch.Tensor) or x.dim() != 4:
-            raise TypeError(f"{name} must be a torch.Tensor of 4 dimensions")
-    if not q.is_cuda:
-        raise ValueError(f"q: on {q.device}, expected a CUDA device")
-    if q.dtype not in _DTYPE_CODE:
-        raise ValueError(f"q: dtype {q.dtype}, expected one of {list(_DTYPE_CODE)}")
-    B, T, Hq, d = q.shape
-    L, Hkv = k.shape[1], k.shape[2]
-    dev, dt = q.device, q.dtype
-    _attn_tensor(q, "q", (B, T, Hq, d), dt, dev)
-    _attn_tensor(k, "k", (B, L, Hkv, d), dt, dev)
-    _attn_tensor(v, "v", (B, L, Hkv, d), dt, dev)
-    P = 0
+def _attention(q, kp, vp, k, v, lens, lens_name, scale, y, lse, workspace, stream):
+    for x, name in ((q, "q"), (k, "k"), (v, "v")):
+        if not isinstance(x, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+    dev, dt, qs, ks = q.device, q.dtype, q.shape, k.shape
+    if dev.type != "cuda":
+        raise ValueError(f"q: on {dev}, expected a CUDA device")
+    _attn_same(k, "k", ks, dt, dev)
+    _attn_same(v, "v", ks, dt, dev)
+    ps = kp_st = vp_st = None
     if kp is not None:
-        if not isinstance(kp, torch.Tensor) or kp.dim() != 3:
-            raise TypeError("k_prefix must be a torch.Tensor of 3 dimensions")
-        P = kp.shape[0]
-        _attn_tensor(kp, "k_prefix", (P, Hkv, d), dt, dev)
-        _attn_tensor(vp, "v_prefix", (P, Hkv, d), dt, dev)
+        if not isinstance(kp, torch.Tensor):
+            raise TypeError("k_prefix must be a torch.Tensor")
+        ps, kp_st = kp.shape, kp.stride()
+        _attn_same(kp, "k_prefix", ps, dt, dev)
+        _attn_same(vp, "v_prefix", ps, dt, dev)
+        vp_st = vp.stride()
+    cfg, need = _attn_plan(qs, ks, ps, q.stride(), k.stride(), v.stride(), kp_st, vp_st, dt, scale)
     if lens is not None:
-        _attn_tensor(lens, lens_name, (B,), torch.int32, dev, packed=True)
+        _attn_same(lens, lens_name, qs[:1], torch.int32, dev, packed=True)
     if y is not None:
-        _attn_tensor(y, "y", (B, T, Hq, d), dt, dev, packed=True)
+        _attn_same(y, "y", qs, dt, dev, packed=True)
     if lse is not None:
-        _attn_tensor(lse, "lse", (B, T, Hq), torch.float32, dev, packed=True)
+        _attn_same(lse, "lse", qs[:3], torch.float32, dev, packed=True)
+    if workspace is not None and not (isinstance(workspace, torch.Tensor) and workspace.dtype == torch.uint8
+                                      and workspace.device == dev and workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
     if stream is not None and stream.device != dev:
         raise ValueError(f"stream: on {stream.device}, expected {dev}")
-    c = LolaAttnConfig(B, T, Hq, Hkv, d, _DTYPE_CODE[dt], P, L, d ** -0.5 if scale is None else scale,
-                       q.stride()[:3], kp.stride()[:2] if P else (0, 0), vp.stride()[:2] if P else (0, 0),
-                       k.stride()[:3], v.stride()[:3])
-    L_ = lib()
-    n = c_size_t()
-    _check(L_.lola_attn_workspace(byref(c), byref(n)))
-    # allocated on the call's own device and stream, so that the allocator orders their reuse after it
-    with torch.cuda.device(dev), torch.cuda.stream(stream):
-        if y is None:
-            y = torch.empty((B, T, Hq, d), dtype=dt, device=dev)
-        if workspace is None:
-            workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
-        elif not (isinstance(workspace, torch.Tensor) and workspace.dtype == torch.uint8 and workspace.device == dev
-                  and workspace.is_contiguous()):
-            raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
-        args = [q.data_ptr()] + ([kp.data_ptr(), vp.data_ptr()] if kp is not None else [])
-        args += [k.data_ptr(), v.data_ptr(), None if lens is None else lens.data_ptr(), y.data_ptr(),
-                 None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                 torch.cuda.current_stream(dev).cuda_stream]
-        _check(getattr(L_, entry)(byref(c), *args))
+    if stream is not None or torch.cuda.current_device() != dev.index:
+        # on the tensors' device and the call's stream, so that the allocator orders the reuse
+        # of what is allocated here behind the call
+        with torch.cuda.device(dev), torch.cuda.stream(stream):
+            return _attn_call(cfg, need, q, kp, vp, k, v, lens, y, lse, workspace)
+    return _attn_call(cfg, need, q, kp, vp, k, v, lens, y, lse, workspace)
+
+
+def _attn_call(cfg, need, q, kp, vp, k, v, lens, y, lse, workspace):
+    if y is None:
+        y = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    ws, size = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    n, ls = 0 if lens is None else lens.data_ptr(), 0 if lse is None else lse.data_ptr()
+    st = torch.cuda.current_stream(q.device.index).cuda_stream      # (without an index it is looked up, slowly)
+    if kp is None:
+        rc = _lib.lola_cross_attention(byref(cfg), q.data_ptr(), k.data_ptr(), v.data_ptr(), n, y.data_ptr(), ls, ws,
+                                       size, st)
+    else:
+        rc = _lib.lola_prefix_attention(byref(cfg), q.data_ptr(), kp.data_ptr(), vp.data_ptr(), k.data_ptr(),
+                                        v.data_ptr(), n, y.data_ptr(), ls, ws, size, st)
+    _check(rc)
     return y
 
 
@@ -247,7 +275,7 @@ def cross_attention(q, k, v, kv_len=None, scale=None, y=None, lse=None, workspac
     (one encoder output for all sequences, read once) among them.  lse (float32 [B,T,Hq]), if
     given, receives each row's log-sum-exp.  workspace: scratch to use instead of an allocation
     (attention_workspace bytes); calls that may overlap need one each."""
-    return _attention("lola_cross_attention", q, None, None, k, v, kv_len, "kv_len", scale, y, lse, workspace, stream)
+    return _attention(q, None, None, k, v, kv_len, "kv_len", scale, y, lse, workspace, stream)
 
 
 def prefix_attention(q, k_prefix, v_prefix, k, v, own_len=None, scale=None, y=None, lse=None, workspace=None,
@@ -259,7 +287,7 @@ def prefix_attention(q, k_prefix, v_prefix, k, v, own_len=None, scale=None, y=No
     t reads the prefix and its own keys s <= own_len[b] - T + t.  The rest as cross_attention."""
     if k_prefix is None or v_prefix is None:
         raise TypeError("k_prefix and v_prefix must be torch.Tensors")
-    return _attention("lola_prefix_attention", q, k_prefix, v_prefix, k, v, own_len, "own_len", scale, y, lse,
+    return _attention(q, k_prefix, v_prefix, k, v, own_len, "own_len", scale, y, lse,
                       workspace, stream)
 
 
