@@ -20,7 +20,7 @@ struct KeySeg {            // one segment of keys; strides in elements
     int n;                               // keys (per sequence)
 };
 
-enum class AttnBy { none, rows, tiles, simple };
+enum class AttnBy { none, rows, tiles };
 
 struct AttnArgs {
     const void* q;
@@ -54,6 +54,10 @@ constexpr int kRowsMax = 32;
 cudaError_t launch_attn_rows(const AttnArgs& a, cudaStream_t s);
 // bf16, any number of rows, 128 keys at a time (attn_tc.cu); packed: the shared keys' group
 cudaError_t launch_attn_tc(const AttnArgs& a, int packed, int num_sms, cudaStream_t s);
+// f32 (attn_f32.cu): up to kF32RowsMax rows of a sequence; any number of rows, packed as above
+constexpr int kF32RowsMax = 16;
+cudaError_t launch_attn_f32_rows(const AttnArgs& a, cudaStream_t s);
+cudaError_t launch_attn_f32_tiles(const AttnArgs& a, int packed, cudaStream_t s);
 cudaError_t attn_error_word(int* word, cudaStream_t s);
 
 // Where row r of a group is: its token over the batch, its offset in q (elements), its index in y.
