@@ -7,27 +7,39 @@
 //
 // Bound: HBM.  It reads each distinct parent once and writes each sequence
 // once; nothing is computed.  A thread owns one column (16 bytes; 4 where a
-// sequence's run is not a multiple of 16) and moves it for many sequences.
+// sequence's run is not a multiple of 16) and moves it for many sequences, eight
+// loads in flight.  B200, the 8B-shaped decode layer (3.2 MB a sequence): one prompt
+// to 64 sequences 37.5 us, 205 MB, 5.5 TB/s (a plain fill of as much takes 31);
+// 44 of 64 beams from 20 survivors in place 57.5 us for 270 MB (decode's residuals
+// included), 4.7 TB/s.  16 loads in flight spill (50 and 96 us); 128-thread CTAs 39
+// and 63; moves sorted by parent so that equal ones share a load 89 in place.
 //
 // * Between two states: loads and stores of kBatch sequences at a time; a run of
 //   sequences with one parent reads it once (samples of a prompt are such a
 //   run), other repeats come from L2.
-// * Inside one state the gather overwrites its own sources, in any pattern
-//   (a swap, a cycle, two children).  The thread that owns a column first
-//   reads it for every sequence that moves into its own shared-memory
-//   slots, then writes them: no barrier, no second buffer and no order of
-//   moves is needed, and sequences that stay are not touched.
+// * Inside one state the gather may overwrite its own sources, in any pattern (a
+//   swap, a cycle, two children).  Sequences that move and are a parent of
+//   another are the hazards: the thread that owns a column first reads it for every
+//   hazard into its own shared-memory slots, then makes the moves, reading
+//   hazards from the slots and all other parents (which stay, or are no
+//   destination) where they lie.  No barrier, no second buffer and no order of
+//   moves is needed, and sequences that stay are not touched.  A search step that
+//   replaces dead beams by survivors has no hazards and runs with every thread; with
+//   many hazards a CTA's first threads share all of its slots.
+#include <limits.h>
+
 #include "lola_internal.h"
 
 namespace lola {
 
 constexpr int kForkBatch = 8;          // sequences in flight per thread
+constexpr int kForkThreads = 256;      // columns of a tile
 
 // The index arithmetic of both kernels: tile -> segment and first column.
 __device__ __forceinline__ const ForkSeg& fork_seg(const ForkArgs& a, long long tile, long long& col0) {
     int i = 0;
     while (i + 1 < a.nseg && tile >= a.seg[i + 1].tile0) ++i;
-    col0 = (tile - a.seg[i].tile0) * a.tile_cols;
+    col0 = (tile - a.seg[i].tile0) * kForkThreads;
     return a.seg[i];
 }
 
@@ -60,7 +72,7 @@ __device__ __forceinline__ void fork_copy_col(const ForkArgs& a, const ForkSeg& 
 }
 
 // Between two states: blockIdx.y picks kForkGroup destination sequences.
-__global__ void __launch_bounds__(256) fork_kernel(const __grid_constant__ ForkArgs a) {
+__global__ void __launch_bounds__(kForkThreads, 3) fork_kernel(const __grid_constant__ ForkArgs a) {
     __shared__ int par[kForkGroup];
     const int b0 = blockIdx.y * kForkGroup, nb = min(kForkGroup, a.n - b0);
     bool bad = false;
@@ -82,91 +94,122 @@ __global__ void __launch_bounds__(256) fork_kernel(const __grid_constant__ ForkA
 }
 
 template <typename V>
-__device__ __forceinline__ void fork_stage_col(const ForkSeg& sg, const int* to, const int* from, int m, V* slot,
-                                               long long col) {
+__device__ __forceinline__ void fork_move_col(const ForkSeg& sg, const int* to, const int* from, int m, const int* hazard,
+                                              int h, V* slot, int nt, long long col) {
     char* base = sg.dst + col * sizeof(V);
-    const int nt = blockDim.x;
+    for (int i0 = 0; i0 < h; i0 += kForkBatch) {
+        V x[kForkBatch];
+#pragma unroll
+        for (int u = 0; u < kForkBatch; ++u)
+            if (i0 + u < h) x[u] = *reinterpret_cast<const V*>(base + hazard[i0 + u] * sg.seq_bytes);
+#pragma unroll
+        for (int u = 0; u < kForkBatch; ++u)
+            if (i0 + u < h) slot[(i0 + u) * nt] = x[u];
+    }
     for (int i0 = 0; i0 < m; i0 += kForkBatch) {
         V x[kForkBatch];
 #pragma unroll
         for (int u = 0; u < kForkBatch; ++u)
-            if (i0 + u < m) x[u] = *reinterpret_cast<const V*>(base + from[i0 + u] * sg.seq_bytes);
+            if (i0 + u < m) {
+                const int p = from[i0 + u];       // a sequence, or -1 - slot
+                x[u] = p >= 0 ? *reinterpret_cast<const V*>(base + p * sg.seq_bytes) : slot[(-1 - p) * nt];
+            }
 #pragma unroll
         for (int u = 0; u < kForkBatch; ++u)
-            if (i0 + u < m) slot[(i0 + u) * nt] = x[u];
+            if (i0 + u < m) *reinterpret_cast<V*>(base + to[i0 + u] * sg.seq_bytes) = x[u];
     }
-    for (int i = 0; i < m; ++i) *reinterpret_cast<V*>(base + to[i] * sg.seq_bytes) = slot[i * nt];
 }
 
-// Inside one state (src == dst).  Shared memory: [n] to, [n] from, then the slots.
-__global__ void fork_in_place_kernel(const __grid_constant__ ForkArgs a) {
+// Inside one state (src == dst).  Shared memory: [n] parent, [n] to, [n] from, [n] hazard, then the slots.
+__global__ void __launch_bounds__(kForkThreads, 2) fork_in_place_kernel(const __grid_constant__ ForkArgs a, int slot_bytes) {
     extern __shared__ __align__(16) unsigned char fork_smem[];
-    __shared__ int moved;
-    const int nt = blockDim.x, tid = threadIdx.x, n4 = (a.n + 3) & ~3;
-    int* to = reinterpret_cast<int*>(fork_smem);
-    int* from = to + n4;
-    unsigned char* slots = fork_smem + 2 * n4 * sizeof(int);
-    if (tid == 0) moved = 0;
-    __syncthreads();
+    __shared__ int moved, hazards;
+    const int tid = threadIdx.x, n4 = (a.n + 3) & ~3;
+    int* par = reinterpret_cast<int*>(fork_smem);
+    int *to = par + n4, *from = to + n4, *hazard = from + n4;
+    unsigned char* slots = fork_smem + 4 * n4 * sizeof(int);
+    if (tid == 0) moved = hazards = 0;
     bool bad = false;
-    for (int b = tid; b < a.n; b += nt) {
+    for (int b = tid; b < a.n; b += kForkThreads) {
         const int p = a.parents[b];
         const bool out = p < 0 || p >= a.src_B;
         bad |= out;
-        if (!out && p != b) {
-            const int i = atomicAdd(&moved, 1);        // any order: the moves are independent once staged
-            to[i] = b;
-            from[i] = p;
-        }
+        par[b] = out ? b : p;
+        to[b] = 0;                                // (until the lists are made: 1 where b is a parent of another)
     }
     fork_flags(a, bad);
     __syncthreads();
-    const int m = moved;
+    for (int b = tid; b < a.n; b += kForkThreads)
+        if (par[b] != b && par[b] < a.n) to[par[b]] = 1;
+    __syncthreads();
+    for (int b = tid; b < a.n; b += kForkThreads) {
+        from[b] = 0;
+        if (to[b] && par[b] != b) {
+            const int i = atomicAdd(&hazards, 1); // any order: slots do not depend on each other
+            hazard[i] = b;
+            from[b] = -1 - i;                     // (for the moment: by sequence)
+        }
+    }
+    __syncthreads();
+    const int h = hazards;
+    // this thread's moves, from the table by sequence to the lists
+    constexpr int kMost = (kForkInPlaceMax + kForkThreads - 1) / kForkThreads;
+    int src[kMost];
+#pragma unroll
+    for (int u = 0; u < kMost; ++u) {
+        const int b = tid + u * kForkThreads;
+        src[u] = b < a.n && par[b] != b ? (par[b] < a.n && from[par[b]] < 0 ? from[par[b]] : par[b]) : INT_MIN;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kMost; ++u)
+        if (src[u] != INT_MIN) {
+            const int i = atomicAdd(&moved, 1);
+            to[i] = tid + u * kForkThreads;
+            from[i] = src[u];
+        }
+    __syncthreads();
+    const int m = moved, width = a.wide ? 16 : 4;
+    int nt = kForkThreads;                        // threads whose slots fit
+    while (nt > 32 && nt * h * width > slot_bytes) nt >>= 1;
+    if (m == 0 || tid >= nt) return;
     for (long long tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
         long long col0;
         const ForkSeg& sg = fork_seg(a, tile, col0);
-        const long long col = col0 + tid;
-        if (col >= sg.cols) continue;
-        if (sg.wide) fork_stage_col(sg, to, from, m, reinterpret_cast<uint4*>(slots) + tid, col);
-        else fork_stage_col(sg, to, from, m, reinterpret_cast<uint32_t*>(slots) + tid, col);
+        const long long end = min(sg.cols, col0 + kForkThreads);
+        for (long long col = col0 + tid; col < end; col += nt) {
+            if (sg.wide) fork_move_col(sg, to, from, m, hazard, h, reinterpret_cast<uint4*>(slots) + tid, nt, col);
+            else fork_move_col(sg, to, from, m, hazard, h, reinterpret_cast<uint32_t*>(slots) + tid, nt, col);
+        }
     }
-}
-
-// The widest in-place launch whose slots fit: 16-byte columns while 32 threads'
-// slots do, else 4-byte columns (n up to kForkInPlaceMax).
-static void in_place_shape(int n, int* threads, int* col_bytes, size_t* smem) {
-    const size_t budget = 200 * 1024, idx = 2 * (size_t)((n + 3) & ~3) * sizeof(int);
-    *col_bytes = 16;
-    *threads = 128;
-    // up to a third of an SM's shared memory per CTA, so that three share it
-    while (*threads > 32 && idx + (size_t)n * *threads * 16 > 68 * 1024) *threads >>= 1;
-    if (idx + (size_t)n * *threads * 16 > budget) *col_bytes = 4;
-    *smem = idx + (size_t)n * *threads * *col_bytes;
 }
 
 cudaError_t launch_fork(ForkArgs a, int num_sms, cudaStream_t s) {
     const bool in_place = a.seg[0].src == a.seg[0].dst;
-    int threads = 256, col_bytes = 16;
-    size_t smem = 0;
-    if (in_place) in_place_shape(a.n, &threads, &col_bytes, &smem);
-    a.tile_cols = threads;
+    // In place every sequence may be a hazard: 32 threads' slots have to fit, 16 bytes wide up to
+    // 200 KB, else 4.  Up to 128 sequences that is the 64 KB with which three CTAs share an SM.
+    size_t slot_bytes = 64 * 1024;
+    a.wide = 1;
+    if ((size_t)a.n * 32 * 16 > 200 * 1024) a.wide = 0;
+    if ((size_t)a.n * 32 * (a.wide ? 16 : 4) > slot_bytes) slot_bytes = (size_t)a.n * 32 * (a.wide ? 16 : 4);
     a.tiles = 0;
     for (int i = 0; i < a.nseg; ++i) {
         ForkSeg& sg = a.seg[i];
-        sg.wide = col_bytes == 16 && sg.seq_bytes % 16 == 0;
+        sg.wide = (a.wide || !in_place) && sg.seq_bytes % 16 == 0;
         sg.cols = sg.seq_bytes / (sg.wide ? 16 : 4);
         sg.tile0 = a.tiles;
-        a.tiles += (sg.cols + threads - 1) / threads;
+        a.tiles += (sg.cols + kForkThreads - 1) / kForkThreads;
     }
-    const long long most = (long long)num_sms * 32;
-    const unsigned gx = (unsigned)(a.tiles < most ? a.tiles : most);
+    auto grid = [&](long long most) { return (unsigned)(a.tiles < most ? a.tiles : most); };
     if (!in_place) {
-        fork_kernel<<<dim3(gx, (a.n + kForkGroup - 1) / kForkGroup), threads, 0, s>>>(a);
+        const int groups = (a.n + kForkGroup - 1) / kForkGroup;
+        fork_kernel<<<dim3(grid((3LL * num_sms + groups - 1) / groups), groups), kForkThreads, 0, s>>>(a);
         return cudaGetLastError();
     }
+    const size_t smem = 4 * (size_t)((a.n + 3) & ~3) * sizeof(int) + slot_bytes;
     cudaError_t e = cudaFuncSetAttribute(fork_in_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    fork_in_place_kernel<<<gx, threads, smem, s>>>(a);
+    fork_in_place_kernel<<<grid(3LL * num_sms), kForkThreads, smem, s>>>(a, (int)slot_bytes);
     return cudaGetLastError();
 }
 

@@ -115,7 +115,7 @@ struct ForkSeg {
     int wide;              // columns of 16 bytes (else 4)
 };
 constexpr int kForkSegs = 13;          // memories a fork may copy
-constexpr int kForkGroup = 16;         // destination sequences per CTA (between two states)
+constexpr int kForkGroup = 64;         // destination sequences per CTA (between two states)
 constexpr int kForkInPlaceMax = 1500;  // sequences of an in-place fork (shared-memory slots, 32 threads x 4 bytes)
 
 struct ForkArgs {
@@ -125,8 +125,8 @@ struct ForkArgs {
     int n, src_B;
     int* src_err;
     int* dst_err;          // bit 1: a parent outside [0, src_B)
-    long long tiles;       // set by the launcher
-    int tile_cols;
+    long long tiles;       // set by the launcher, as
+    int wide;              // in place: 16-byte slots (else 4)
 };
 
 // Sets the text of lola_last_error_string and returns code; adds to lola_launch_count.
