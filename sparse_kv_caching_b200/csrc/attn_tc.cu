@@ -242,7 +242,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
     } else {
         // ---- queries: 128-byte swizzled, block kb holds dims 64 kb .. 64 kb + 63 of every row ----
         constexpr int NC = DIM / 8;
-        const int w = tid - 320;
         unsigned nq[2] = {0, 0};
         bool ok = true;
         for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
@@ -252,12 +251,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                 if (nq[t]) ok = tc_wait(&mbar[Sh::QFREE + t], (nq[t] - 1) & 1, abort_flag);
                 ++nq[t];
                 if (!ok) break;
-                for (int idx = w; idx < kTcRows * NC; idx += 64) {
-                    const int r = idx / NC, c = idx % NC, R = x.r0 + t * kTcRows + r;
-                    const bool in = R < x.R;
-                    const RowAt y = row_at(a, x.n0, x.g, in ? R : 0);
-                    umma::cp_async16_zfill(sQ + t * Sh::QB + (c >> 3) * (kTcRows * 128) + umma::sw128_off(r, c & 7),
-                                           (const bf16*)a.q + y.q + 8 * c, in);
+                // each lane finds one row, then 32 / NC rows at a time are copied in 16-byte chunks
+#pragma unroll 1
+                for (int r32 = 32 * (warp - 10); r32 < kTcRows; r32 += 64) {
+                    const int R = x.r0 + t * kTcRows + r32 + lane;
+                    const long long at = R < x.R ? row_at(a, x.n0, x.g, R).q : -1;
+#pragma unroll
+                    for (int k = 0; k < NC; ++k) {
+                        const int rr = k * (32 / NC) + lane / NC, c = lane % NC, r = r32 + rr;
+                        const long long from = __shfl_sync(0xffffffffu, at, rr);
+                        umma::cp_async16_zfill(sQ + t * Sh::QB + (c >> 3) * (kTcRows * 128) + umma::sw128_off(r, c & 7),
+                                               (const bf16*)a.q + (from < 0 ? 0 : from) + 8 * c, from >= 0);
+                    }
                 }
                 umma::cp_async_commit();
             }
@@ -326,20 +331,28 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                         umma::tmem_st16(tO + c, o);
                     }
                 }
-                float sum0 = 0.f, sum1 = 0.f;
+                const unsigned long long cc = f2pack(c2, c2), rr = f2pack(-ref, -ref), ones = f2pack(1.f, 1.f);
+                unsigned long long sum[2] = {0ull, 0ull};
 #pragma unroll
                 for (int c = 0; c < kTcKeys; c += 32) {
                     uint32_t w[16];
 #pragma unroll
                     for (int u = 0; u < 16; ++u) {
-                        const float e0 = tc_ex2(fmaf(s[c + 2 * u], c2, -ref)), e1 = tc_ex2(fmaf(s[c + 2 * u + 1], c2, -ref));
-                        sum0 += e0;
-                        sum1 += e1;
+                        float e0, e1;
+                        f2unpack(f2fma(f2pack(s[c + 2 * u], s[c + 2 * u + 1]), cc, rr), e0, e1);
+                        e0 = tc_ex2(e0);
+                        e1 = tc_ex2(e1);
+                        sum[u & 1] = f2fma(f2pack(e0, e1), ones, sum[u & 1]);
                         w[u] = tc_pack(e0, e1);
                     }
                     umma::tmem_st16(tS + c / 2, *reinterpret_cast<const float(*)[16]>(w));
                 }
-                l += sum0 + sum1;
+                {
+                    float x0, x1, x2, x3;
+                    f2unpack(sum[0], x0, x1);
+                    f2unpack(sum[1], x2, x3);
+                    l += (x0 + x1) + (x2 + x3);
+                }
                 if (t == 0 && !sh && x.len < a.own.n && k0 + kTcKeys > x.len) {
                     // rows of V behind the sequence's length may hold anything: 0 x NaN is not 0
                     const unsigned nv = n + 2 * (j - x.j0) + 1;
