@@ -88,6 +88,31 @@ __device__ __forceinline__ void tc_expect(uint64_t* mbar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" :: "r"(umma::smem_addr(mbar)), "r"(bytes) : "memory");
 }
 
+// The products' warp runs as a whole, so that its control flow and the operand descriptors are
+// the same in all lanes (the instructions take them from warp-wide registers); `on` is set in the
+// one lane that issues.
+__device__ __forceinline__ void tc_mma_ss(uint32_t on, uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n"
+        :: "r"(d), "l"(a), "l"(b), "r"(id), "r"(acc), "r"(on));
+}
+__device__ __forceinline__ void tc_mma_ts(uint32_t on, uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n"
+        :: "r"(d), "r"(a), "l"(b), "r"(id), "r"(acc), "r"(on));
+}
+__device__ __forceinline__ void tc_commit(uint32_t on, uint64_t* mbar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n"
+        :: "r"(umma::smem_addr(mbar)), "r"(on) : "memory");
+}
+__device__ __forceinline__ bool tc_wait_warp(uint64_t* mbar, uint32_t parity, volatile int* abort) {
+    return __all_sync(0xffffffffu, tc_wait(mbar, parity, abort));
+}
+
 // One work item: up to 256 rows of a group against a range of key tiles.
 struct TcItem {
     int g, b, n0, R, r0, part;      // kv head, sequence, first token, rows of the group, first row, part
@@ -173,7 +198,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
         }
     } else if (warp == 9) {
         // ---- products ----
-        if (lane == 0) {
+        {
+            const uint32_t on = lane == 0;
             const uint32_t idS = umma::idesc(umma::kBF16, kTcRows, kTcKeys, false, false);
             const uint32_t idO = umma::idesc(umma::kBF16, kTcRows, DIM, false, true);
             const uint64_t dQ = umma::sdesc_sw128(umma::smem_addr(sQ), 16, 1024);
@@ -185,15 +211,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
 #pragma unroll
                 for (int ks = 0; ks < DIM / 16; ++ks) {
                     const uint64_t step = (uint64_t)((ks >> 2) * kTcRows * 8 + (ks & 3) * 2);
-                    umma::mma_bf16(tmem + Sh::TS + 128 * t, q + step, k + step, idS, ks > 0);
+                    tc_mma_ss(on, tmem + Sh::TS + 128 * t, q + step, k + step, idS, ks > 0);
                 }
-                umma::commit(&mbar[Sh::SFULL + t]);
+                tc_commit(on, &mbar[Sh::SFULL + t]);
             };
             auto values = [&](int t, int s, bool first) {
                 const uint64_t v = dV + (uint64_t)(s * (Sh::ST / 16));
 #pragma unroll
                 for (int ks = 0; ks < kTcKeys / 16; ++ks)
-                    umma::mma_f16_ts(tmem + Sh::TO + 128 * t, tmem + Sh::TS + 128 * t + 8 * ks, v + (uint64_t)(ks * 128),
+                    tc_mma_ts(on, tmem + Sh::TO + 128 * t, tmem + Sh::TS + 128 * t + 8 * ks, v + (uint64_t)(ks * 128),
                                      idO, ks > 0 || !first);
             };
             unsigned n = 0, np[2] = {0, 0}, nq[2] = {0, 0};
@@ -202,41 +228,41 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                 const TcItem x = tc_item(p, i);
                 const int nt = x.j1 - x.j0, nr = x.two ? 2 : 1;
                 if (nt == 0) continue;
-                auto full = [&](unsigned m) { return tc_wait(&mbar[Sh::FULL + m % NST], (m / NST) & 1, abort_flag); };
+                auto full = [&](unsigned m) { return tc_wait_warp(&mbar[Sh::FULL + m % NST], (m / NST) & 1, abort_flag); };
                 ok = full(n);
                 for (int t = 0; t < nr && ok; ++t) {
-                    ok = tc_wait(&mbar[Sh::QFULL + t], nq[t] & 1, abort_flag);
+                    ok = tc_wait_warp(&mbar[Sh::QFULL + t], nq[t] & 1, abort_flag);
                     ++nq[t];
                     if (!ok) break;
                     umma::fence_after_sync();
                     scores(t, n % NST);
-                    if (nt == 1) umma::commit(&mbar[Sh::QFREE + t]);
+                    if (nt == 1) tc_commit(on, &mbar[Sh::QFREE + t]);
                 }
                 if (!ok) break;
-                umma::commit(&mbar[Sh::FREE + n % NST]);
+                tc_commit(on, &mbar[Sh::FREE + n % NST]);
                 for (int j = 0; j < nt && ok; ++j) {
                     const unsigned nv = n + 2 * j + 1, nk = nv + 1;
                     const bool more = j + 1 < nt;
                     ok = full(nv);
                     for (int t = 0; t < nr && ok; ++t) {
-                        ok = tc_wait(&mbar[Sh::PFULL + t], np[t] & 1, abort_flag);
+                        ok = tc_wait_warp(&mbar[Sh::PFULL + t], np[t] & 1, abort_flag);
                         ++np[t];
                         if (!ok) break;
                         umma::fence_after_sync();
                         values(t, nv % NST, j == 0);
-                        if (!more) { umma::commit(&mbar[Sh::OFULL + t]); continue; }
+                        if (!more) { tc_commit(on, &mbar[Sh::OFULL + t]); continue; }
                         if (t == 0) ok = full(nk);
                         if (!ok) break;
                         scores(t, nk % NST);
-                        if (j + 2 == nt) umma::commit(&mbar[Sh::QFREE + t]);
+                        if (j + 2 == nt) tc_commit(on, &mbar[Sh::QFREE + t]);
                     }
                     if (!ok) break;
-                    umma::commit(&mbar[Sh::FREE + nv % NST]);
-                    if (more) umma::commit(&mbar[Sh::FREE + nk % NST]);
+                    tc_commit(on, &mbar[Sh::FREE + nv % NST]);
+                    if (more) tc_commit(on, &mbar[Sh::FREE + nk % NST]);
                 }
                 n += 2 * nt;
             }
-            umma::commit(&mbar[Sh::DONE]);        // nothing may be in flight when tensor memory is given back
+            tc_commit(on, &mbar[Sh::DONE]);        // nothing may be in flight when tensor memory is given back
             if (!umma::mbar_wait(&mbar[Sh::DONE], 0, 4000000000ull)) *abort_flag = 1;
         }
     } else {
