@@ -49,12 +49,13 @@ struct TcArgs {
 
 template <int DIM>
 struct TcShape {
-    static constexpr int QB = kTcRows * DIM * 2, ST = kTcKeys * DIM * 2, NST = DIM == 128 ? 5 : 8;
+    static constexpr int QB = kTcRows * DIM * 2, ST = kTcKeys * DIM * 2, NST = 4;
     static constexpr int Q = 0, RING = 2 * QB, MBAR = RING + NST * ST;
     static constexpr int NBAR = 2 * NST + 11;
     static constexpr int FLAG = MBAR + NBAR * 8, BYTES = FLAG + 16 + 1024;
     static_assert(BYTES <= 227 * 1024, "shared memory");
-    static constexpr uint32_t TS = 0, TO = 256;       // + 128 per row tile
+    // tensor memory, all 512 columns of it: S (and P) of row tile t at 128 t, O at 256 + 128 t
+    static constexpr uint32_t TS = 0, TO = 256;
     // barriers
     static constexpr int FULL = 0, FREE = NST, QFULL = 2 * NST, QFREE = QFULL + 2, SFULL = QFREE + 2,
                          PFULL = SFULL + 2, OFULL = PFULL + 2, DONE = OFULL + 2;
@@ -62,12 +63,14 @@ struct TcShape {
 
 __device__ __forceinline__ bool tc_wait(uint64_t* mbar, uint32_t parity, volatile int* abort) {
     if (umma::mbar_try_wait(mbar, parity)) return true;
-    const uint64_t t0 = umma::globaltimer_ns();
-    while (!umma::mbar_try_wait(mbar, parity)) {
-        if (*abort) return false;
-        if (umma::globaltimer_ns() - t0 > 4000000000ull) { *abort = 1; return false; }
+    const long long t0 = clock64();               // (globaltimer takes too long to read for a wait this short)
+    for (unsigned n = 1;; ++n) {
+        if (umma::mbar_try_wait(mbar, parity)) return true;
+        if ((n & 63) == 0) {
+            if (*abort) return false;
+            if (clock64() - t0 > 8000000000ll) { *abort = 1; return false; }
+        }
     }
-    return true;
 }
 __device__ __forceinline__ float tc_ex2(float x) {
     float y;
@@ -88,27 +91,18 @@ __device__ __forceinline__ void tc_expect(uint64_t* mbar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" :: "r"(umma::smem_addr(mbar)), "r"(bytes) : "memory");
 }
 
-// The products' warp runs as a whole, so that its control flow and the operand descriptors are
-// the same in all lanes (the instructions take them from warp-wide registers); `on` is set in the
-// one lane that issues.
-__device__ __forceinline__ void tc_mma_ss(uint32_t on, uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n"
-        :: "r"(d), "l"(a), "l"(b), "r"(id), "r"(acc), "r"(on));
+// The products' warp runs as a whole and elects the lane that issues, and every operand of a
+// product is a constant or the same in all lanes (the ring's stage, the row tile and the tensor
+// memory's columns are constants of the code that issues): the compiler then keeps them in
+// warp-wide registers, where the instruction takes them.  With operands that it has to move there
+// each product costs several more instructions, and beside the two busy softmax warps on the same
+// scheduler 16 products of 128 x 128 x 16 took 1900 cycles instead of 1280 (1025 alone).
+__device__ __forceinline__ bool tc_elect() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(p));
+    return p != 0;
 }
-__device__ __forceinline__ void tc_mma_ts(uint32_t on, uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n"
-        :: "r"(d), "r"(a), "l"(b), "r"(id), "r"(acc), "r"(on));
-}
-__device__ __forceinline__ void tc_commit(uint32_t on, uint64_t* mbar) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n"
-        :: "r"(umma::smem_addr(mbar)), "r"(on) : "memory");
-}
+template <int V> struct TcInt { static constexpr int v = V; };
 __device__ __forceinline__ bool tc_wait_warp(uint64_t* mbar, uint32_t parity, volatile int* abort) {
     return __all_sync(0xffffffffu, tc_wait(mbar, parity, abort));
 }
@@ -170,7 +164,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
     umma::fence_before_sync();
     __syncthreads();
     umma::fence_after_sync();
-    const uint32_t tmem = *tptr;
+    const uint32_t tmem = *tptr;                // all of tensor memory: column 0
+    if (tid == 0 && tmem != 0) *abort_flag = 1;
     // registers: 256 x 208 + 128 x 88 = the 384 x 168 of the launch
     if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
@@ -198,73 +193,99 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
         }
     } else if (warp == 9) {
         // ---- products ----
-        {
-            const uint32_t on = lane == 0;
-            const uint32_t idS = umma::idesc(umma::kBF16, kTcRows, kTcKeys, false, false);
-            const uint32_t idO = umma::idesc(umma::kBF16, kTcRows, DIM, false, true);
-            const uint64_t dQ = umma::sdesc_sw128(umma::smem_addr(sQ), 16, 1024);
-            const uint64_t dK = umma::sdesc_sw128(umma::smem_addr(ring), 16, 1024);
-            const uint64_t dV = umma::sdesc_sw128(umma::smem_addr(ring), kTcKeys * 128, 1024);
-            // Q and K: a step of 16 dims is 32 bytes inside a 128-byte half row, the next half 128 rows on
-            auto scores = [&](int t, int s) {
-                const uint64_t q = dQ + (uint64_t)(t * (Sh::QB / 16)), k = dK + (uint64_t)(s * (Sh::ST / 16));
+        constexpr uint32_t idS = umma::idesc(umma::kBF16, kTcRows, kTcKeys, false, false);
+        constexpr uint32_t idO = umma::idesc(umma::kBF16, kTcRows, DIM, false, true);
+        const uint64_t dQ = umma::sdesc_sw128(umma::smem_addr(sQ), 16, 1024);
+        const uint64_t dK = umma::sdesc_sw128(umma::smem_addr(ring), 16, 1024);
+        const uint64_t dV = umma::sdesc_sw128(umma::smem_addr(ring), kTcKeys * 128, 1024);
+        // S of row tile T from the key tile in stage ST.  Q and K: a step of 16 dims is 32 bytes inside
+        // a 128-byte half row, the next half 128 rows on.
+        auto scores = [&](auto T, auto ST, bool last) {
+            constexpr int t = decltype(T)::v, st = decltype(ST)::v;
+            if (!tc_elect()) return;
+            constexpr int q0 = t * (Sh::QB / 16), k0 = st * (Sh::ST / 16);
+            // (a loop of few registers: unrolled, its descriptors would all be kept across the loop over the tiles)
+#pragma unroll 1
+            for (int h = 0; h < DIM / 64; ++h)
 #pragma unroll
-                for (int ks = 0; ks < DIM / 16; ++ks) {
-                    const uint64_t step = (uint64_t)((ks >> 2) * kTcRows * 8 + (ks & 3) * 2);
-                    tc_mma_ss(on, tmem + Sh::TS + 128 * t, q + step, k + step, idS, ks > 0);
+                for (int ks = 0; ks < 4; ++ks) {
+                    const int step = h * kTcRows * 8 + ks * 2;
+                    umma::mma_bf16(Sh::TS + 128 * t, dQ + (uint64_t)(q0 + step), dK + (uint64_t)(k0 + step), idS, h + ks > 0);
                 }
-                tc_commit(on, &mbar[Sh::SFULL + t]);
-            };
-            auto values = [&](int t, int s, bool first) {
-                const uint64_t v = dV + (uint64_t)(s * (Sh::ST / 16));
+            umma::commit(&mbar[Sh::SFULL + t]);
+            if (last) umma::commit(&mbar[Sh::QFREE + t]);
+        };
+        // O of row tile T (+)= P V, V in stage ST
+        auto values = [&](auto T, auto ST, bool first, bool last) {
+            constexpr int t = decltype(T)::v, st = decltype(ST)::v;
+            if (!tc_elect()) return;
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int ks = 0; ks < kTcKeys / 16; ++ks)
-                    tc_mma_ts(on, tmem + Sh::TO + 128 * t, tmem + Sh::TS + 128 * t + 8 * ks, v + (uint64_t)(ks * 128),
+                for (int k4 = 0; k4 < kTcKeys / 32; ++k4) {
+                    const int ks = h * (kTcKeys / 32) + k4;
+                    umma::mma_f16_ts(Sh::TO + 128 * t, Sh::TS + 128 * t + 8 * ks, dV + (uint64_t)(st * (Sh::ST / 16) + ks * 128),
                                      idO, ks > 0 || !first);
+                }
+            if (last) umma::commit(&mbar[Sh::OFULL + t]);
+        };
+        auto release = [&](auto ST) {
+            if (tc_elect()) umma::commit(&mbar[Sh::FREE + decltype(ST)::v]);
+        };
+        auto wait = [&](int i, unsigned parity) { return tc_wait_warp(&mbar[i], parity & 1, abort_flag); };
+        // Key tile number g of this CTA sits in stages 2 (g % 2) and 2 (g % 2) + 1.
+        unsigned g = 0, np[2] = {0, 0}, nq[2] = {0, 0};
+        bool ok = true;
+        // the first scores of an item
+        auto open = [&](auto PAR, int nr, int nt) {
+            constexpr int par = decltype(PAR)::v;
+            ok = wait(Sh::FULL + 2 * par, g >> 1);
+            auto row_tile = [&](auto T) {
+                constexpr int t = decltype(T)::v;
+                if (t >= nr || !ok) return;
+                ok = wait(Sh::QFULL + t, nq[t]++);
+                if (!ok) return;
+                umma::fence_after_sync();
+                scores(TcInt<t>{}, TcInt<2 * par>{}, nt == 1);
             };
-            unsigned n = 0, np[2] = {0, 0}, nq[2] = {0, 0};
-            bool ok = true;
-            for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
-                const TcItem x = tc_item(p, i);
-                const int nt = x.j1 - x.j0, nr = x.two ? 2 : 1;
-                if (nt == 0) continue;
-                auto full = [&](unsigned m) { return tc_wait_warp(&mbar[Sh::FULL + m % NST], (m / NST) & 1, abort_flag); };
-                ok = full(n);
-                for (int t = 0; t < nr && ok; ++t) {
-                    ok = tc_wait_warp(&mbar[Sh::QFULL + t], nq[t] & 1, abort_flag);
-                    ++nq[t];
-                    if (!ok) break;
-                    umma::fence_after_sync();
-                    scores(t, n % NST);
-                    if (nt == 1) tc_commit(on, &mbar[Sh::QFREE + t]);
-                }
-                if (!ok) break;
-                tc_commit(on, &mbar[Sh::FREE + n % NST]);
-                for (int j = 0; j < nt && ok; ++j) {
-                    const unsigned nv = n + 2 * j + 1, nk = nv + 1;
-                    const bool more = j + 1 < nt;
-                    ok = full(nv);
-                    for (int t = 0; t < nr && ok; ++t) {
-                        ok = tc_wait_warp(&mbar[Sh::PFULL + t], np[t] & 1, abort_flag);
-                        ++np[t];
-                        if (!ok) break;
-                        umma::fence_after_sync();
-                        values(t, nv % NST, j == 0);
-                        if (!more) { tc_commit(on, &mbar[Sh::OFULL + t]); continue; }
-                        if (t == 0) ok = full(nk);
-                        if (!ok) break;
-                        scores(t, nk % NST);
-                        if (j + 2 == nt) tc_commit(on, &mbar[Sh::QFREE + t]);
-                    }
-                    if (!ok) break;
-                    tc_commit(on, &mbar[Sh::FREE + nv % NST]);
-                    if (more) tc_commit(on, &mbar[Sh::FREE + nk % NST]);
-                }
-                n += 2 * nt;
+            row_tile(TcInt<0>{});
+            row_tile(TcInt<1>{});
+            if (ok) release(TcInt<2 * par>{});
+        };
+        // values of tile j (parity PAR) and scores of the next, row tile by row tile
+        auto step = [&](auto PAR, int nr, int nt, int j) {
+            constexpr int par = decltype(PAR)::v;
+            const bool more = j + 1 < nt;
+            ok = wait(Sh::FULL + 2 * par + 1, g >> 1);
+            if (more && ok) ok = wait(Sh::FULL + 2 * (1 - par), (g + 1) >> 1);
+            auto row_tile = [&](auto T) {
+                constexpr int t = decltype(T)::v;
+                if (t >= nr || !ok) return;
+                ok = wait(Sh::PFULL + t, np[t]++);
+                if (!ok) return;
+                umma::fence_after_sync();
+                values(TcInt<t>{}, TcInt<2 * par + 1>{}, j == 0, !more);
+                if (more) scores(TcInt<t>{}, TcInt<2 * (1 - par)>{}, j + 2 == nt);
+            };
+            row_tile(TcInt<0>{});
+            row_tile(TcInt<1>{});
+            if (!ok) return;
+            release(TcInt<2 * par + 1>{});
+            if (more) release(TcInt<2 * (1 - par)>{});
+        };
+        for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
+            const TcItem x = tc_item(p, i);
+            const int nt = x.j1 - x.j0, nr = x.two ? 2 : 1;
+            if (nt == 0) continue;
+            if (g & 1) open(TcInt<1>{}, nr, nt);
+            else open(TcInt<0>{}, nr, nt);
+            for (int j = 0; j < nt && ok; ++j, ++g) {
+                if (g & 1) step(TcInt<1>{}, nr, nt, j);
+                else step(TcInt<0>{}, nr, nt, j);
             }
-            tc_commit(on, &mbar[Sh::DONE]);        // nothing may be in flight when tensor memory is given back
-            if (!umma::mbar_wait(&mbar[Sh::DONE], 0, 4000000000ull)) *abort_flag = 1;
         }
+        if (tc_elect()) umma::commit(&mbar[Sh::DONE]);        // nothing may be in flight when tensor memory is given back
+        if (!umma::mbar_wait(&mbar[Sh::DONE], 0, 4000000000ull)) *abort_flag = 1;
     } else {
         // ---- queries: 128-byte swizzled, block kb holds dims 64 kb .. 64 kb + 63 of every row ----
         constexpr int NC = DIM / 8;
@@ -272,6 +293,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
         bool ok = true;
         for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
             const TcItem x = tc_item(p, i);
+            if (i + gridDim.x < p.items) {
+                // the next item's rows into L2 meanwhile: its copies start when this item's last scores are
+                // made, and the products wait for them
+                const TcItem y = tc_item(p, i + gridDim.x);
+                for (int R = y.r0 + tid - 320; R < min(y.R, y.r0 + 2 * kTcRows); R += 64) {
+                    const bf16* q = (const bf16*)a.q + row_at(a, y.n0, y.g, R).q;
+#pragma unroll
+                    for (int c = 0; c < DIM; c += 64) asm volatile("prefetch.global.L2 [%0];" :: "l"(q + c));
+                }
+            }
             if (x.j0 == x.j1) continue;
             for (int t = 0; t < (x.two ? 2 : 1) && ok; ++t) {
                 if (nq[t]) ok = tc_wait(&mbar[Sh::QFREE + t], (nq[t] - 1) & 1, abort_flag);
@@ -335,10 +366,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
 #pragma unroll
                     for (int u = 0; u < kTcKeys; ++u) s[u] = u < lim ? s[u] : -INFINITY;
                 }
-                float mx = fmaxf(s[0], s[1]);
+                float m4[4] = {s[0], s[1], s[2], s[3]};      // four chains: the latency of one would show
 #pragma unroll
-                for (int u = 2; u < kTcKeys; u += 2) mx = fmaxf(mx, fmaxf(s[u], s[u + 1]));
-                mx *= c2;
+                for (int u = 4; u < kTcKeys; u += 8)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) m4[v] = fmaxf(m4[v], u + 4 < kTcKeys ? fmaxf(s[u + v], s[u + v + 4]) : s[u + v]);
+                float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c2;
                 float f = 1.f;
                 bool raise = false;
                 if (m == -INFINITY) m = mx;       // nothing read yet
