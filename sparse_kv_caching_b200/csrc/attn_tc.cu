@@ -50,7 +50,7 @@ struct TcArgs {
 template <int DIM>
 struct TcShape {
     static constexpr int QB = kTcRows * DIM * 2, ST = kTcKeys * DIM * 2, NST = 4;
-    static constexpr int Q = 0, RING = 2 * QB, MBAR = RING + NST * ST;
+    static constexpr int Q = 0, RING = 2 * QB, OUT = RING + NST * ST, MBAR = OUT + 8 * 2048;    // OUT: 32 rows x 64 bytes per warp
     static constexpr int NBAR = 2 * NST + 11;
     static constexpr int FLAG = MBAR + NBAR * 8, BYTES = FLAG + 16 + 1024;
     static_assert(BYTES <= 227 * 1024, "shared memory");
@@ -349,8 +349,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             if (t == 1 && !x.two) { n += 2 * (x.j1 - x.j0); continue; }
             const int R = x.r0 + t * kTcRows + r;
             const bool row_ok = R < x.R;
-            const RowAt at = row_at(a, x.n0, x.g, row_ok ? R : 0);
-            const int vis = row_ok ? own_visible(a, x.len, at.t) : 0, vis0 = row_ok ? a.shared.n : 0;
+            const int vis = row_ok ? own_visible(a, x.len, row_at(a, x.n0, x.g, R).t) : 0, vis0 = row_ok ? a.shared.n : 0;
             float m = -INFINITY, l = 0.f;
             for (int j = x.j0; j < x.j1; ++j, ++ns) {
                 bool ok = tc_wait(&mbar[Sh::SFULL + t], ns & 1, abort_flag);
@@ -440,33 +439,64 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             }
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const float l2 = l == 0.f ? -INFINITY : m + log2f(l);
-            const size_t rows_all = (size_t)a.B * a.T * a.Hq, po = (size_t)(p.part0 + x.part) * rows_all + at.o;
+            // The row's place is found again: kept across the loop it would cost registers there.
+            int Ro = row_ok ? R : 0;
+            asm volatile("" : "+r"(Ro));
+            const size_t at = row_at(a, x.n0, x.g, Ro).o;
+            const size_t po = (size_t)(p.part0 + x.part) * a.B * a.T * a.Hq + at;
+            uint8_t* to = !row_ok ? nullptr
+                          : a.part_o ? reinterpret_cast<uint8_t*>(a.part_o + po * DIM)
+                                     : reinterpret_cast<uint8_t*>((bf16*)a.y + at * DIM);
+            // Rows leave through shared memory, 64 bytes at a time, so that four lanes write one row's: a
+            // thread that wrote its own row would touch 32 lines with every instruction, and the
+            // barriers of the next item would wait behind those stores.
+            uint8_t* out = smem + Sh::OUT + warp * 2048;
+            auto leave = [&](int c, const uint32_t (&w)[16]) {
 #pragma unroll
-            for (int c = 0; c < DIM; c += 32) {
-                float o[32];
+                for (int u = 0; u < 4; ++u)
+                    *reinterpret_cast<uint4*>(out + lane * 64 + ((u ^ (lane >> 1 & 3)) << 4)) =
+                        make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+                __syncwarp();
+#pragma unroll
+                for (int it = 0; it < 4; ++it) {
+                    const int rr = 8 * it + (lane >> 2), u = lane & 3;
+                    const unsigned long long row = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), rr);
+                    if (row)
+                        *reinterpret_cast<uint4*>(row + 64 * c + 16 * u) =
+                            *reinterpret_cast<const uint4*>(out + rr * 64 + ((u ^ (rr >> 1 & 3)) << 4));
+                }
+                __syncwarp();
+            };
+#pragma unroll 1
+            for (int c = 0; c < DIM / 16; ++c) {
+                float o[16];
+                uint32_t w[16];
                 if (any) {
-                    umma::tmem_ld16(tO + c, *reinterpret_cast<float(*)[16]>(o));
-                    umma::tmem_ld16(tO + c + 16, *reinterpret_cast<float(*)[16]>(o + 16));
+                    umma::tmem_ld16(tO + 16 * c, o);
                     umma::tmem_wait_ld();
                 }
 #pragma unroll
-                for (int u = 0; u < 32; ++u) o[u] = l == 0.f ? 0.f : o[u] * inv;
-                if (!row_ok) continue;
+                for (int u = 0; u < 16; ++u) o[u] = l == 0.f ? 0.f : o[u] * inv;
                 if (a.part_o) {
-#pragma unroll
-                    for (int u = 0; u < 32; u += 4)
-                        *reinterpret_cast<float4*>(a.part_o + po * DIM + c + u) = make_float4(o[u], o[u + 1], o[u + 2], o[u + 3]);
+                    leave(c, *reinterpret_cast<const uint32_t(*)[16]>(o));
                 } else {
 #pragma unroll
-                    for (int u = 0; u < 32; u += 8)
-                        *reinterpret_cast<uint4*>((bf16*)a.y + at.o * DIM + c + u) =
-                            make_uint4(tc_pack(o[u], o[u + 1]), tc_pack(o[u + 2], o[u + 3]), tc_pack(o[u + 4], o[u + 5]),
-                                       tc_pack(o[u + 6], o[u + 7]));
+                    for (int u = 0; u < 8; ++u) w[u] = tc_pack(o[2 * u], o[2 * u + 1]);
+                    ++c;
+                    if (any) {
+                        umma::tmem_ld16(tO + 16 * c, o);
+                        umma::tmem_wait_ld();
+                    }
+#pragma unroll
+                    for (int u = 0; u < 16; ++u) o[u] = l == 0.f ? 0.f : o[u] * inv;
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) w[8 + u] = tc_pack(o[2 * u], o[2 * u + 1]);
+                    leave(c >> 1, w);
                 }
             }
             if (row_ok) {
                 if (a.part_o) a.part_l[po] = l2;
-                else if (a.lse) a.lse[at.o] = l2 * 0.6931471805599453f;
+                else if (a.lse) a.lse[at] = l2 * 0.6931471805599453f;
             }
         }
     }
