@@ -19,28 +19,74 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
     const size_t rows = (size_t)a.B * a.T * a.Hq, row = (size_t)blockIdx.x * 4 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     if (row >= rows) return;
-    const int np = a.parts_own + a.parts_shared;
+    // parts in part_o: [p0, p1); of a group whose rounds were dealt evenly and that a cut goes through
+    // (k = 0 shared, 1 own): the slots of CTAs c0 .. c1 instead
+    int p0 = 0, p1 = a.parts_shared + a.parts_own;
+    int total = 0, runs = 0, gb[2] = {0, 0}, c0[2] = {0, 0}, c1[2] = {-1, -1}, rr[2] = {0, 0}, g = 0;
+    if (a.even) {
+        const int h = (int)(row % a.Hq), n = (int)(row / a.Hq), b = n / a.T;
+        g = h / a.Gq;
+        const bool own = a.by_own == AttnBy::rows;
+        const int sh = a.by_shared == AttnBy::rows ? (a.shared.n + kRwRound - 1) / kRwRound : 0;
+        total = sh + (own ? a.goff[a.B] : 0);
+        runs = min(a.even, total);
+        auto cta = [&](int x) { return (int)(((x + 1LL) * runs - 1) / total); };
+        if (sh) {
+            c0[0] = 0;
+            c1[0] = cta(sh - 1);
+            rr[0] = n * a.Gq + h % a.Gq;
+            if (c1[0] == 0) c1[0] = -1;
+            else p0 = 1;
+        }
+        if (own) {
+            const int o = a.goff[b], len = a.goff[b + 1] - o;
+            gb[1] = sh + o;
+            c0[1] = cta(gb[1]);
+            c1[1] = cta(gb[1] + len - 1);
+            rr[1] = (n - b * a.T) * a.Gq + h % a.Gq;
+            if (c0[1] == c1[1]) c1[1] = -1;
+            else p1 = a.parts_shared;
+        }
+        if (!a.part_o) {
+            if (c1[1] < 0) return;             // written whole
+            p1 = p0;
+        }
+    }
     float m = -INFINITY;
-    for (int p = lane; p < np; p += 32) m = fmaxf(m, a.part_l[p * rows + row]);
+    for (int p = p0 + lane; p < p1; p += 32) m = fmaxf(m, a.part_l[p * rows + row]);
+    auto slot = [&](int k, int c) {
+        const bool second = c == c0[k] && (int)((long long)total * c / runs) != gb[k];     // not the group that CTA's run begins in
+        return (size_t)(2 * (c * a.Hkv + g) + second) * a.slot_rows + rr[k];
+    };
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        for (int c = c0[k] + lane; c <= c1[k]; c += 32) m = fmaxf(m, a.slot_l[slot(k, c)]);
     m = warp_max(m);
     const float ref = m == -INFINITY ? 0.f : m;
     float sum = 0.f, acc[EPL];
 #pragma unroll
     for (int u = 0; u < EPL; ++u) acc[u] = 0.f;
-#pragma unroll 4
-    for (int p = 0; p < np; ++p) {
-        const float w = exp2f(a.part_l[p * rows + row] - ref);
-        const float* o = a.part_o + (p * rows + row) * DIM + lane * EPL;
+    auto add = [&](const float* po, float pl) {
+        const float w = exp2f(pl - ref);
         sum += w;
         if (EPL == 4) {
-            const float4 x = *reinterpret_cast<const float4*>(o);
+            const float4 x = *reinterpret_cast<const float4*>(po);
             acc[0] = fmaf(w, x.x, acc[0]); acc[1] = fmaf(w, x.y, acc[1]);
             acc[EPL - 2] = fmaf(w, x.z, acc[EPL - 2]); acc[EPL - 1] = fmaf(w, x.w, acc[EPL - 1]);
         } else {
-            const float2 x = *reinterpret_cast<const float2*>(o);
+            const float2 x = *reinterpret_cast<const float2*>(po);
             acc[0] = fmaf(w, x.x, acc[0]); acc[1] = fmaf(w, x.y, acc[1]);
         }
-    }
+    };
+#pragma unroll 8
+    for (int p = p0; p < p1; ++p) add(a.part_o + (p * rows + row) * DIM + lane * EPL, a.part_l[p * rows + row]);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll 4
+        for (int c = c0[k]; c <= c1[k]; ++c) {
+            const size_t q = slot(k, c);
+            add(a.slot_o + q * DIM + lane * EPL, a.slot_l[q]);
+        }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
     for (int u = 0; u < EPL; ++u) store_as((TOut*)a.y + row * DIM + lane * EPL + u, acc[u] * inv);
@@ -50,7 +96,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
 size_t plan_attn(AttnArgs& a, int num_sms) {
     a.walk = 1;
     a.by_shared = a.by_own = AttnBy::none;
-    a.parts_shared = a.parts_own = a.chunk_shared = a.chunk_own = 0;
+    a.parts_shared = a.parts_own = a.chunk_shared = a.chunk_own = a.even = a.slot_rows = 0;
     const bool f32 = a.dtype == 0;
     const int rows = a.T * a.Gq, P = a.shared.n, L = a.own.n;
     const long long groups = (long long)a.B * a.Hkv, all_rows = (long long)a.B * rows;
@@ -65,13 +111,7 @@ size_t plan_attn(AttnArgs& a, int num_sms) {
         if (*chunk == 0) *chunk = unit;
         *parts = n > 0 ? (int)tiles(n, *chunk) : 1;
     };
-    // Two CTAs per SM of the kernels for few rows, parts of at least 256 keys: four rounds of a CTA;
-    // f32 tiles: two per SM, parts of 128 keys; bf16 tiles: one per SM, four tiles of 128 keys.
-    auto cut_rows = [&](long long n, long long ctas, int* parts, int* chunk) {
-        long long c;
-        cut(n, ctas, 2LL * num_sms, 64, f32 ? 128 : 256, parts, &c);
-        *chunk = (int)c;
-    };
+    // f32: two CTAs per SM, parts of at least 128 keys; bf16 tiles: one per SM, four tiles of 128 keys.
     auto cut_tiles = [&](long long n0, long long n1, long long r, long long heads, int* parts, int* chunk) {
         long long c;
         if (f32) {
@@ -97,28 +137,68 @@ size_t plan_attn(AttnArgs& a, int num_sms) {
             a.walk = a.B * tiles(rows, of) < 2 * tiles(all_rows, of);
         }
     }
+    const int n0 = a.walk ? P : 0;              // shared keys that a sequence's rows read before their own
     if (!a.walk) {
         if (all_rows <= few && !f32) {
             a.by_shared = AttnBy::rows;
-            cut_rows(P, a.Hkv, &a.parts_shared, &a.chunk_shared);
+            a.parts_shared = 1;
         } else {
             a.by_shared = AttnBy::tiles;
             cut_tiles(P, 0, all_rows, a.Hkv, &a.parts_shared, &a.chunk_shared);
         }
     }
     if (a.walk || L > 0) {
-        const int n0 = a.walk ? P : 0;
-        if (rows <= few) {
-            a.by_own = AttnBy::rows;
-            cut_rows((long long)n0 + L, groups * (f32 ? tiles(rows, 4) : 1), &a.parts_own, &a.chunk_own);
-        } else {
+        if (rows > few) {
             a.by_own = AttnBy::tiles;
             cut_tiles(n0, L, rows, groups, &a.parts_own, &a.chunk_own);
+        } else {
+            a.by_own = AttnBy::rows;
+            a.parts_own = 1;
+            if (f32) {
+                long long c;
+                cut((long long)n0 + L, groups * tiles(rows, 4), 2LL * num_sms, 32, 128, &a.parts_own, &c);
+                a.chunk_own = (int)c;
+            }
         }
     }
+    if (!f32 && (a.by_own == AttnBy::rows || a.by_shared == AttnBy::rows)) {
+        // Rounds of 64 keys, a CTA per group or dealt evenly?  In rounds: a CTA on an SM of its own or with
+        // one neighbour takes about one unit of time for each, and four for its begin and end; evenly
+        // dealt work needs the join, about four more.
+        const long long slots = 2LL * num_sms;
+        const long long sh = a.by_shared == AttnBy::rows ? tiles(P, kRwRound) : 0;
+        const long long own = a.by_own == AttnBy::rows ? tiles((long long)n0 + L, kRwRound) : 0;
+        const long long ctas = (sh ? a.Hkv : 0) + (own ? groups : 0), all = sh + own * a.B;      // of one head
+        const long long most = sh > own ? sh : own, runs = slots / a.Hkv < all ? slots / a.Hkv : all;
+        if (runs > 0 && all < (1LL << 30) && tiles(all, runs) + 8 < tiles(ctas, slots) * (most + 4)) a.even = (int)runs;
+        a.slot_rows = (int)(sh ? all_rows : rows);
+    }
     const int parts = a.parts_own + a.parts_shared;
-    if (parts == 1) return 0;
-    return (size_t)parts * a.B * a.T * a.Hq * (a.d + 1) * 4;
+    size_t bytes = 0;
+    auto take = [&](size_t n) { bytes += (n + 255) & ~(size_t)255; };
+    if (parts > 1) take((size_t)parts * a.B * a.T * a.Hq * (a.d + 1) * 4);
+    if (a.even) {
+        take((size_t)2 * a.even * a.Hkv * a.slot_rows * (a.d + 1) * 4);
+        take(((size_t)a.B + 1) * 4);
+    }
+    return bytes;
+}
+
+void place_attn(AttnArgs& a, void* workspace) {
+    char* w = (char*)workspace;
+    const int parts = a.parts_own + a.parts_shared;
+    auto take = [&](size_t n) { char* p = w; w += (n + 255) & ~(size_t)255; return p; };
+    if (parts > 1) {
+        const size_t rows = (size_t)parts * a.B * a.T * a.Hq;
+        a.part_o = (float*)take(rows * (a.d + 1) * 4);
+        a.part_l = a.part_o + rows * a.d;
+    }
+    if (a.even) {
+        const size_t rows = (size_t)2 * a.even * a.Hkv * a.slot_rows;
+        a.slot_o = (float*)take(rows * (a.d + 1) * 4);
+        a.slot_l = a.slot_o + rows * a.d;
+        a.goff = (int*)take(((size_t)a.B + 1) * 4);
+    }
 }
 
 cudaError_t launch_attn(const AttnArgs& a, int num_sms, int* launches, cudaStream_t s) {
@@ -138,7 +218,7 @@ cudaError_t launch_attn(const AttnArgs& a, int num_sms, int* launches, cudaStrea
     if ((a.by_shared == AttnBy::rows || a.by_own == AttnBy::rows) &&
         !run(f32 ? launch_attn_f32_rows(a, s) : launch_attn_rows(a, s)))
         return e;
-    if (a.part_o) {
+    if (a.part_o || a.even) {
         const unsigned grid = (unsigned)(((size_t)a.B * a.T * a.Hq + 3) / 4);
         if (f32) {
             if (a.d == 128) attn_join_kernel<128, float><<<grid, 128, 0, s>>>(a);

@@ -43,14 +43,22 @@ struct AttnArgs {
     int chunk_shared, chunk_own;       // keys per part
     float* part_o;         // [parts][B T Hq][d]
     float* part_l;         // [parts][B T Hq]
+    // attn_rows_kernel with each kv head's rounds dealt evenly to this many CTAs (0: a CTA per group): what is
+    // left of groups that a cut goes through, and the rounds before each sequence
+    int even, slot_rows;
+    float* slot_o;         // [even][Hkv][2][slot_rows][d]
+    float* slot_l;         // [even][Hkv][2][slot_rows]
+    int* goff;             // [B + 1]
 };
+constexpr int kRwRound = 64;           // keys of a round
 
 // Chooses how the keys are cut (every field after scale_log2 but the pointers) and returns the
 // bytes of workspace that needs.
 size_t plan_attn(AttnArgs& a, int num_sms);
+void place_attn(AttnArgs& a, void* workspace);       // sets the pointers into it
 cudaError_t launch_attn(const AttnArgs& a, int num_sms, int* launches, cudaStream_t s);
 // bf16, up to kRowsMax rows per group (attn_rows.cu); the parts of both kinds that are its own
-constexpr int kRowsMax = 32;
+constexpr int kRowsMax = 16;
 cudaError_t launch_attn_rows(const AttnArgs& a, cudaStream_t s);
 // bf16, any number of rows, 128 keys at a time (attn_tc.cu); packed: the shared keys' group
 cudaError_t launch_attn_tc(const AttnArgs& a, int packed, int num_sms, cudaStream_t s);

@@ -109,10 +109,7 @@ int run(const lola_attn_config* c, int causal, const void* q, const void* kp, co
     a.shared.k = kp; a.shared.v = vp;
     a.own.k = k; a.own.v = v;
     a.own_len = len;
-    if (need) {
-        a.part_o = (float*)workspace;
-        a.part_l = a.part_o + need / ((a.d + 1) * 4) * a.d;
-    }
+    lola::place_attn(a, workspace);
     int launches = 0;
     const cudaError_t e = lola::launch_attn(a, sms, &launches, (cudaStream_t)stream);
     if (e != cudaSuccess) return report(LOLA_ERR_CUDA, "attention kernel: %s", cudaGetErrorString(e));

@@ -1,24 +1,33 @@
 // Exact attention for few rows per kv head (decode steps, short drafts), bf16.
 //
-// A group's R <= 32 rows (queries x heads of the kv group) read N keys: 4 R d N
+// A group's R <= 16 rows (queries x heads of the kv group) read N keys: 4 R d N
 // operations on 4 d N bytes, R operations a byte, so the kernel is bound by HBM
 // as long as each key is read once for all its rows and enough loads are in
-// flight.  One warp owns 16-key blocks (every kRwWarps-th of its CTA's range): it
-// copies a block's K and V rows into its own ring of stages with cp.async two
-// blocks ahead and never waits for another warp; S = Q K^T and O += P V run on
-// the warp-level tensor instructions (m16n8k16: 16-row tiles of Q in registers,
-// which a tile of 128 rows on the SM-level unit would leave almost empty).
-// Softmax: running maximum and sum per row and warp, f32; the accumulator is
-// rescaled only when a maximum rises.  P is fed as two bf16 parts (its rounding
-// and the remainder): the second product is free under the loads and keeps the
-// weights to 2^-16.  At the end the warps' (m, l, O) meet in shared memory.
-// Rows of V that no query of the group may read are filled with zeros.
+// flight.  Keys go by rounds of 64, 16 for each of a CTA's four warps: a warp copies
+// its 16 K and V rows into its own ring of stages with cp.async two rounds ahead
+// and waits for no other warp; S = Q K^T and O += P V run on the warp-level tensor
+// instructions (m16n8k16: a 16-row tile of Q in registers, which a tile of 128 rows
+// on the SM-level unit would leave almost empty).  Softmax: running maximum and
+// sum per row and warp, f32; the accumulator is rescaled only when a maximum
+// rises.  P is fed as two bf16 parts (its rounding and the remainder): the second
+// product is free under the loads and keeps the weights to 2^-16.
+//
+// How the rounds are dealt (plan_attn).  Whole: a CTA per group, which then writes y
+// itself.  Even: for each kv head the rounds of all its groups in one list, cut into
+// equal runs for two CTAs per SM, whatever the sequences' lengths; the copies of a run
+// do not stop where one group ends and the next begins.  The heads' lists are cut
+// alike and their CTAs start together, so that the rows of one token, which lie next to
+// each other, are read at about the same time.  A group that lies inside a run is written
+// whole; what a CTA has of a group that a cut goes through is left in one of its two slots
+// (the group its run begins in, the one it ends in), and attn_join_kernel puts the
+// slots together.
 #include "attn.h"
 #include "umma.cuh"
 
 namespace lola {
 
 constexpr int kRwWarps = 4, kRwKeys = 16, kRwStages = 3;
+static_assert(kRwRound == kRwWarps * kRwKeys, "a round");
 
 __device__ __forceinline__ void rw_ldsm(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -48,256 +57,338 @@ __device__ __forceinline__ void rw_split(float x0, float x1, uint32_t& hi, uint3
     lo = rw_pack(x0 - __uint_as_float(hi << 16), x1 - __uint_as_float(hi & 0xFFFF0000u));
 }
 
-template <int DIM, int MT>
+template <int DIM>
 struct RowsShape {
     static constexpr int STAGE = 2 * kRwKeys * DIM * 2;               // K rows, then V rows
     static constexpr int WARP = kRwStages * STAGE;
-    static constexpr int RED = MT * 16 * DIM * 4;                     // one warp's O, at the end
-    static constexpr int BYTES = kRwWarps * WARP + kRwWarps * MT * 16 * 8;
-    static_assert(RED <= WARP, "the stages hold a warp's O");
+    static constexpr int RED = kRwWarps * WARP;                       // 8 rows of every warp's O where a group ends
+    static constexpr int ML = RED + kRwWarps * 8 * DIM * 4, SCAN = ML + kRwWarps * 8 * 8, BYTES = SCAN + 64;
 };
 
-template <int DIM, int MT>
-__global__ void __launch_bounds__(kRwWarps * 32) attn_rows_kernel(const __grid_constant__ AttnArgs a) {
-    using Sh = RowsShape<DIM, MT>;
+// A place in a kv head's list of rounds: first the shared keys' group (where this kernel reads
+// them apart), then each sequence's.
+struct RowsAt {
+    int shared, b, round, rounds;
+};
+
+__device__ __forceinline__ int rw_rounds(const AttnArgs& a, int b) {  // of one group of sequence b
+    return max(1, (int)(((a.walk ? a.shared.n : 0) + (long long)own_length(a, b) + kRwRound - 1) / kRwRound));
+}
+__device__ __forceinline__ void rw_next(const AttnArgs& a, RowsAt& x) {
+    if (++x.round < x.rounds) return;
+    x.round = 0;
+    x.b = x.shared ? 0 : x.b + 1;
+    x.shared = 0;
+    if (x.b < a.B) x.rounds = rw_rounds(a, x.b);
+}
+
+template <int DIM>
+__global__ void __launch_bounds__(kRwWarps * 32, 2) attn_rows_kernel(const __grid_constant__ AttnArgs a) {
+    using Sh = RowsShape<DIM>;
     using bf16 = __nv_bfloat16;
     constexpr int KC = DIM / 8;                 // 16-byte chunks of a key row
     constexpr int RB = DIM * 2;                 // its bytes
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = blockIdx.x % a.Hkv, run = blockIdx.x / a.Hkv;
 
-    // ---- which rows, which keys ----
-    const int n_sh = a.by_shared == AttnBy::rows ? a.parts_shared * a.Hkv : 0;      // CTAs of the shared group
-    int g, b = 0, part, lo, hi, n0, R, np0;     // np0: keys of the walk that are shared ones
-    if ((int)blockIdx.x < n_sh) {
-        part = blockIdx.x % a.parts_shared;
-        g = blockIdx.x / a.parts_shared;
-        n0 = 0;
-        R = a.B * a.T * a.Gq;
-        np0 = a.shared.n;
-        lo = part * a.chunk_shared;
-        hi = (int)min((long long)np0, (long long)lo + a.chunk_shared);
+    // ---- this CTA's run of rounds ----
+    RowsAt at{};                                // where it begins
+    int left;                                   // rounds
+    const int sh_rounds = a.by_shared == AttnBy::rows ? (a.shared.n + kRwRound - 1) / kRwRound : 0;
+    if (!a.even) {
+        at.shared = sh_rounds && run == 0;
+        at.b = at.shared ? 0 : run - (sh_rounds ? 1 : 0);
+        at.rounds = at.shared ? sh_rounds : rw_rounds(a, at.b);
+        left = at.rounds;
     } else {
-        int i = blockIdx.x - n_sh;
-        part = i % a.parts_own;
-        i /= a.parts_own;
-        g = i % a.Hkv;
-        b = i / a.Hkv;
-        n0 = b * a.T;
-        R = a.T * a.Gq;
-        np0 = a.walk ? a.shared.n : 0;
-        lo = part * a.chunk_own;
-        hi = (int)min((long long)np0 + own_length(a, b), (long long)lo + a.chunk_own);
-        part += a.parts_shared;
-    }
-    const int len = (int)blockIdx.x < n_sh ? 0 : own_length(a, b);
-    const bf16* ksh = (const bf16*)a.shared.k + (long long)g * a.shared.kh;
-    const bf16* vsh = (const bf16*)a.shared.v + (long long)g * a.shared.vh;
-    const bf16* kow = (const bf16*)a.own.k + b * a.own.kb + (long long)g * a.own.kh;
-    const bf16* vow = (const bf16*)a.own.v + b * a.own.vb + (long long)g * a.own.vh;
-
-    uint8_t* ring = smem + warp * Sh::WARP;
-    const int nblk = max(0, (hi - lo + kRwKeys - 1) / kRwKeys);
-    const int mine = nblk > warp ? (nblk - warp + kRwWarps - 1) / kRwWarps : 0;
-    // copy block j of this warp into its stage: lanes take one 16-byte chunk of a row each
-    auto fetch = [&](int j) {
-        uint8_t* st = ring + (j % kRwStages) * Sh::STAGE;
-        const int k0 = lo + (warp + j * kRwWarps) * kRwKeys;
-        constexpr int RPI = 32 / KC;            // rows per pass
+        // rounds before each sequence (goff): every CTA sums them, the first one leaves them for the join
+        int* scan = reinterpret_cast<int*>(smem + Sh::SCAN);
+        const int own = a.by_own == AttnBy::rows, nb = own ? a.B : 0;
+        const int per = (nb + kRwWarps * 32 - 1) / (kRwWarps * 32), b0 = min(nb, tid * per), b1 = min(nb, b0 + per);
+        int mine = 0;
+        for (int b = b0; b < b1; ++b) mine += rw_rounds(a, b);
+        int incl = mine;
 #pragma unroll
-        for (int it = 0; it < kRwKeys / RPI; ++it) {
-            const int r = it * RPI + lane / KC, c = lane % KC, key = k0 + r;
-            const bool ok = key < hi, sh = key < np0;
-            const long long i = ok ? (sh ? key : key - np0) : 0;
-            const bf16* kp = (sh ? ksh + i * a.shared.ks : kow + i * a.own.ks) + 8 * c;
-            const bf16* vp = (sh ? vsh + i * a.shared.vs : vow + i * a.own.vs) + 8 * c;
-            const uint32_t off = r * RB + ((c ^ (r & 7)) << 4);
-            umma::cp_async16_zfill(st + off, ok ? (const void*)kp : a.q, ok);
-            umma::cp_async16_zfill(st + kRwKeys * RB + off, ok ? (const void*)vp : a.q, ok);
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
         }
-    };
-#pragma unroll
-    for (int j = 0; j < kRwStages - 1; ++j) {
-        if (j < mine) fetch(j);
-        umma::cp_async_commit();
-    }
-
-    // ---- queries: A fragments of 16-row tiles (row lane/4 and + 8, dims 2 (lane%4) and + 8) ----
-    uint32_t qf[MT][DIM / 16][4];
-    int lim[MT][2];                             // keys of the walk that each of this lane's rows reads
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-            const int r = mt * 16 + hh * 8 + lane / 4;
-            const bool ok = r < R;
-            const RowAt x = row_at(a, n0, g, ok ? r : 0);
-            const uint32_t* qp = reinterpret_cast<const uint32_t*>((const bf16*)a.q + x.q) + lane % 4;
-            lim[mt][hh] = np0 + own_visible(a, len, x.t);
-#pragma unroll
-            for (int kk = 0; kk < DIM / 16; ++kk) {
-                qf[mt][kk][hh] = ok ? qp[8 * kk] : 0u;
-                qf[mt][kk][hh + 2] = ok ? qp[8 * kk + 4] : 0u;
+        if (lane == 31) scan[warp] = incl;
+        __syncthreads();
+        int before = incl - mine, all = 0;
+        for (int w = 0; w < kRwWarps; ++w) {
+            if (w < warp) before += scan[w];
+            all += scan[w];
+        }
+        const int total = sh_rounds + all, runs = min(a.even, total), c = min(run, runs);
+        const int begin = (int)((long long)total * c / runs), end = (int)((long long)total * min(c + 1, runs) / runs);
+        left = end - begin;
+        if (blockIdx.x == 0) {
+            int o = before;
+            for (int b = b0; b < b1; ++b) {
+                a.goff[b] = o;
+                o += rw_rounds(a, b);
+            }
+            if (tid == 0) a.goff[a.B] = all;
+        }
+        if (begin >= sh_rounds) {
+            const int x = begin - sh_rounds;
+            int o = before;
+            for (int b = b0; b < b1; ++b) {
+                const int n = rw_rounds(a, b);
+                if (x >= o && x < o + n) {
+                    scan[8] = b;
+                    scan[9] = x - o;
+                    scan[10] = n;
+                }
+                o += n;
             }
         }
+        __syncthreads();
+        if (begin < sh_rounds) at = {1, 0, begin, sh_rounds};
+        else at = {0, scan[8], scan[9], scan[10]};
+    }
+    if (left == 0) return;
 
-    float o[MT][DIM / 8][4], m[MT][2], l[MT][2];
+    // ---- copies, two rounds ahead of the products ----
+    uint8_t* ring = smem + warp * Sh::WARP;
+    RowsAt ahead = at;
+    int to_fetch = left;
+    int stage_in = 0;
+    const bf16 *fk = nullptr, *fv = nullptr;    // this lane's chunk of key 0 of the group, shared or own
+    const bf16 *sk = nullptr, *sv = nullptr;    // ... of the shared keys, in front of the own ones (walk)
+    int np0 = 0, n_keys = 0;
+    long long fks = 0, fvs = 0;
+    auto enter = [&] {                          // pointers of the group `ahead` is in
+        const int c = 8 * (lane % KC);
+        const KeySeg& sg = ahead.shared ? a.shared : a.own;
+        fk = (const bf16*)sg.k + ahead.b * sg.kb + (long long)g * sg.kh + c;
+        fv = (const bf16*)sg.v + ahead.b * sg.vb + (long long)g * sg.vh + c;
+        fks = sg.ks;
+        fvs = sg.vs;
+        np0 = !ahead.shared && a.walk ? a.shared.n : 0;
+        if (np0) {
+            sk = (const bf16*)a.shared.k + (long long)g * a.shared.kh + c;
+            sv = (const bf16*)a.shared.v + (long long)g * a.shared.vh + c;
+        }
+        n_keys = ahead.shared ? a.shared.n : np0 + own_length(a, ahead.b);
+    };
+    enter();
+    auto fetch = [&] {
+        if (to_fetch > 0) {
+            uint8_t* st = ring + stage_in * Sh::STAGE;
+            const int k0 = ahead.round * kRwRound + warp * kRwKeys;
+            constexpr int RPI = 32 / KC;        // rows per pass
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+            for (int it = 0; it < kRwKeys / RPI; ++it) {
+                const int r = it * RPI + lane / KC, c = lane % KC, key = k0 + r;
+                const bool ok = key < n_keys;
+                const bf16* kp = fk + (key - np0) * fks;
+                const bf16* vp = fv + (key - np0) * fvs;
+                if (key < np0) {
+                    kp = sk + key * a.shared.ks;
+                    vp = sv + key * a.shared.vs;
+                }
+                const uint32_t off = r * RB + ((c ^ (r & 7)) << 4);
+                umma::cp_async16_zfill(st + off, ok ? (const void*)kp : a.q, ok);
+                umma::cp_async16_zfill(st + kRwKeys * RB + off, ok ? (const void*)vp : a.q, ok);
+            }
+            stage_in = stage_in + 1 == kRwStages ? 0 : stage_in + 1;
+            const bool last = ahead.round + 1 == ahead.rounds;
+            rw_next(a, ahead);
+            if (--to_fetch > 0 && last) enter();
+        }
+        umma::cp_async_commit();
+    };
+#pragma unroll
+    for (int j = 0; j < kRwStages - 1; ++j) fetch();
+
+    // ---- queries: A fragments (row lane/4 and + 8, dims 2 (lane%4) and + 8) ----
+    uint32_t qf[DIM / 16][4];
+    int lim[2];                                 // keys of the group that each of this lane's rows reads
+    int R = 0, n0 = 0;
+    auto queries = [&](const RowsAt& x) {
+        n0 = x.shared ? 0 : x.b * a.T;
+        R = (x.shared ? a.B : 1) * a.T * a.Gq;
+        const int len = x.shared ? 0 : own_length(a, x.b), ns = x.shared || a.walk ? a.shared.n : 0;
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+            const int r = hh * 8 + lane / 4;
+            const bool ok = r < R;
+            const RowAt y = row_at(a, n0, g, ok ? r : 0);
+            const uint32_t* qp = reinterpret_cast<const uint32_t*>((const bf16*)a.q + y.q) + lane % 4;
+            lim[hh] = ns + (x.shared ? 0 : own_visible(a, len, y.t));
+#pragma unroll
+            for (int kk = 0; kk < DIM / 16; ++kk) {
+                qf[kk][hh] = ok ? qp[8 * kk] : 0u;
+                qf[kk][hh + 2] = ok ? qp[8 * kk + 4] : 0u;
+            }
+        }
+    };
+    queries(at);
+
+    float o[DIM / 8][4], m[2], l[2];
+    auto clear = [&] {
 #pragma unroll
         for (int n = 0; n < DIM / 8; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[mt][n][i] = 0.f;
-        m[mt][0] = m[mt][1] = -INFINITY;
-        l[mt][0] = l[mt][1] = 0.f;
-    }
+            for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.f;
+    };
+    clear();
     const uint32_t ring_s = umma::smem_addr(ring);
     // ldmatrix addresses: lane i gives row (i % 8) of 8 x 8 matrix i / 8
     const int krow = (lane & 7) + ((lane >> 4) << 3), kch = (lane >> 3) & 1;      // K: matrices (keys, dims) 00 01 10 11
     const int vrow = (lane & 7) + (((lane >> 3) & 1) << 3), vch = lane >> 4;      // V: (keys, dims) 00 10 01 11
-    for (int j = 0; j < mine; ++j) {
+    int stage = 0, from = at.round;             // `from`: this CTA's first round of the group
+    bool first_group = true;
+    for (; left > 0; --left) {
         umma::cp_async_wait<kRwStages - 2>();
         __syncwarp();
-        if (j + kRwStages - 1 < mine) fetch(j + kRwStages - 1);       // into the stage read at j - 1
-        umma::cp_async_commit();
-        const uint32_t ks = ring_s + (j % kRwStages) * Sh::STAGE, vs = ks + kRwKeys * RB;
-        const int k0 = lo + (warp + j * kRwWarps) * kRwKeys;
-        float s[MT][2][4];
+        fetch();                                // into the stage read one round ago
+        const uint32_t ks = ring_s + stage * Sh::STAGE, vs = ks + kRwKeys * RB;
+        stage = stage + 1 == kRwStages ? 0 : stage + 1;
+        const int k0 = at.round * kRwRound + warp * kRwKeys;
+        float s[2][4];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[mt][0][i] = s[mt][1][i] = 0.f;
+        for (int i = 0; i < 4; ++i) s[0][i] = s[1][i] = 0.f;
 #pragma unroll
         for (int kk = 0; kk < DIM / 16; ++kk) {
             uint32_t kf[4];
             rw_ldsm(kf, ks + krow * RB + (((2 * kk + kch) ^ (krow & 7)) << 4));
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                rw_mma(s[mt][0], qf[mt][kk], kf[0], kf[1]);
-                rw_mma(s[mt][1], qf[mt][kk], kf[2], kf[3]);
-            }
+            rw_mma(s[0], qf[kk], kf[0], kf[1]);
+            rw_mma(s[1], qf[kk], kf[2], kf[3]);
         }
-        uint32_t ph[MT][4], pl[MT][4];
+        uint32_t ph[4], pl[4];
+        float f[2];
+        bool up = false;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            float f[2];
-            bool up = false;
+        for (int hh = 0; hh < 2; ++hh) {
+            // this lane's keys: 2 (lane % 4) + {0, 1} of each 8-key tile
+            float x[4], mx = -INFINITY;
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-                // this lane's keys: 2 (lane % 4) + {0, 1} of each 8-key tile
-                float x[4], mx = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int key = k0 + (i >> 1) * 8 + 2 * (lane & 3) + (i & 1);
-                    x[i] = key < min(lim[mt][hh], hi) ? s[mt][i >> 1][2 * hh + (i & 1)] * a.scale_log2 : -INFINITY;
-                    mx = fmaxf(mx, x[i]);
-                }
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                const float mn = fmaxf(m[mt][hh], mx), ref = mn == -INFINITY ? 0.f : mn;
-                f[hh] = rw_ex2(m[mt][hh] - ref);
-                up |= mn != m[mt][hh];
-                m[mt][hh] = mn;
-                float sum = 0.f;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    x[i] = rw_ex2(x[i] - ref);
-                    sum += x[i];
-                }
-                l[mt][hh] = l[mt][hh] * f[hh] + sum;                  // this lane's keys only: summed over lanes at the end
-                rw_split(x[0], x[1], ph[mt][hh], pl[mt][hh]);         // A fragment: keys 2 (lane%4), then + 8
-                rw_split(x[2], x[3], ph[mt][hh + 2], pl[mt][hh + 2]);
+            for (int i = 0; i < 4; ++i) {
+                const int key = k0 + (i >> 1) * 8 + 2 * (lane & 3) + (i & 1);
+                x[i] = key < lim[hh] ? s[i >> 1][2 * hh + (i & 1)] * a.scale_log2 : -INFINITY;
+                mx = fmaxf(mx, x[i]);
             }
-            if (__any_sync(0xffffffffu, up)) {
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            const float mn = fmaxf(m[hh], mx), ref = mn == -INFINITY ? 0.f : mn;
+            f[hh] = rw_ex2(m[hh] - ref);
+            up |= mn != m[hh];
+            m[hh] = mn;
+            float sum = 0.f;
 #pragma unroll
-                for (int n = 0; n < DIM / 8; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) o[mt][n][i] *= f[i >> 1];
+            for (int i = 0; i < 4; ++i) {
+                x[i] = rw_ex2(x[i] - ref);
+                sum += x[i];
             }
+            l[hh] = l[hh] * f[hh] + sum;                  // this lane's keys only: summed over lanes at the end
+            rw_split(x[0], x[1], ph[hh], pl[hh]);         // A fragment: keys 2 (lane%4), then + 8
+            rw_split(x[2], x[3], ph[hh + 2], pl[hh + 2]);
+        }
+        if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+            for (int n = 0; n < DIM / 8; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[n][i] *= f[i >> 1];
         }
 #pragma unroll
         for (int n2 = 0; n2 < DIM / 16; ++n2) {
             uint32_t vf[4];
             rw_ldsm_t(vf, vs + vrow * RB + (((2 * n2 + vch) ^ (vrow & 7)) << 4));
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                rw_mma(o[mt][2 * n2], ph[mt], vf[0], vf[1]);
-                rw_mma(o[mt][2 * n2 + 1], ph[mt], vf[2], vf[3]);
-                rw_mma(o[mt][2 * n2], pl[mt], vf[0], vf[1]);
-                rw_mma(o[mt][2 * n2 + 1], pl[mt], vf[2], vf[3]);
-            }
+            rw_mma(o[2 * n2], ph, vf[0], vf[1]);
+            rw_mma(o[2 * n2 + 1], ph, vf[2], vf[3]);
+            rw_mma(o[2 * n2], pl, vf[0], vf[1]);
+            rw_mma(o[2 * n2 + 1], pl, vf[2], vf[3]);
         }
-    }
+        const bool group_ends = at.round + 1 == at.rounds;
+        if (!group_ends && left > 1) {
+            ++at.round;
+            continue;
+        }
 
-    // ---- the warps' sums meet: O in the (free) stages, m and l behind them ----
-    umma::cp_async_wait<0>();
-    __syncwarp();
-    float* red = reinterpret_cast<float*>(ring);
-    float2* ml = reinterpret_cast<float2*>(smem + kRwWarps * Sh::WARP);
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+        // ---- the group, or the run, ends: the warps' sums meet, 8 rows at a time ----
+        const RowsAt done = at;
+        const int R_done = R, n0_done = n0;
+        rw_next(a, at);
+        if (left > 1) queries(at);              // (their loads fly while the sums meet)
+        const bool whole = from == 0 && group_ends;
+        const size_t rows_all = (size_t)a.B * a.T * a.Hq;
+        const int part = done.shared ? 0 : a.parts_shared, slot = 2 * (int)blockIdx.x + (first_group ? 0 : 1);
+        float* red = reinterpret_cast<float*>(smem + Sh::RED);
+        float2* ml = reinterpret_cast<float2*>(smem + Sh::ML);
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
-            float x = l[mt][hh];
+            const int r0 = hh * 8;
+            if (r0 >= R_done) break;
+            float x = l[hh];
             x += __shfl_xor_sync(0xffffffffu, x, 1);
             x += __shfl_xor_sync(0xffffffffu, x, 2);
-            const int r = mt * 16 + hh * 8 + lane / 4;
-            if ((lane & 3) == 0) ml[warp * MT * 16 + r] = make_float2(m[mt][hh], x);
-            if (r < R) {
+            if ((lane & 3) == 0) ml[warp * 8 + lane / 4] = make_float2(m[hh], x);
+            if (r0 + lane / 4 < R_done) {
 #pragma unroll
                 for (int n = 0; n < DIM / 8; ++n)
-                    *reinterpret_cast<float2*>(red + r * DIM + 8 * n + 2 * (lane & 3)) =
-                        make_float2(o[mt][n][2 * hh], o[mt][n][2 * hh + 1]);
+                    *reinterpret_cast<float2*>(red + (warp * 8 + lane / 4) * DIM + 8 * n + 2 * (lane & 3)) =
+                        make_float2(o[n][2 * hh], o[n][2 * hh + 1]);
             }
-        }
-    __syncthreads();
-    const bool whole = a.part_o == nullptr;
-    const size_t rows_all = (size_t)a.B * a.T * a.Hq;
-    for (int i = tid; i < R * (DIM / 4); i += kRwWarps * 32) {
-        const int r = i / (DIM / 4), c = i % (DIM / 4) * 4;
-        float mx = -INFINITY;
+            __syncthreads();
+            for (int i = tid; i < min(8, R_done - r0) * (DIM / 4); i += kRwWarps * 32) {
+                const int r = i / (DIM / 4), c = i % (DIM / 4) * 4;
+                float mx = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kRwWarps; ++w) mx = fmaxf(mx, ml[w * MT * 16 + r].x);
-        const float ref = mx == -INFINITY ? 0.f : mx;
-        float sum = 0.f;
-        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int w = 0; w < kRwWarps; ++w) mx = fmaxf(mx, ml[w * 8 + r].x);
+                const float ref = mx == -INFINITY ? 0.f : mx;
+                float sum = 0.f;
+                float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < kRwWarps; ++w) {
-            const float2 z = ml[w * MT * 16 + r];
-            const float f = rw_ex2(z.x - ref);
-            const float4 x = *reinterpret_cast<const float4*>(smem + w * Sh::WARP + (r * DIM + c) * 4);
-            sum = fmaf(z.y, f, sum);
-            y.x = fmaf(x.x, f, y.x); y.y = fmaf(x.y, f, y.y); y.z = fmaf(x.z, f, y.z); y.w = fmaf(x.w, f, y.w);
+                for (int w = 0; w < kRwWarps; ++w) {
+                    const float2 z = ml[w * 8 + r];
+                    const float f = rw_ex2(z.x - ref);
+                    const float4 v = *reinterpret_cast<const float4*>(red + (w * 8 + r) * DIM + c);
+                    sum = fmaf(z.y, f, sum);
+                    y.x = fmaf(v.x, f, y.x); y.y = fmaf(v.y, f, y.y); y.z = fmaf(v.z, f, y.z); y.w = fmaf(v.w, f, y.w);
+                }
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                y.x *= inv; y.y *= inv; y.z *= inv; y.w *= inv;
+                const float l2 = sum == 0.f ? -INFINITY : ref + log2f(sum);
+                const size_t at_y = row_at(a, n0_done, g, r0 + r).o;
+                if (!whole) {
+                    const size_t q = (size_t)slot * a.slot_rows + r0 + r;
+                    *reinterpret_cast<float4*>(a.slot_o + q * DIM + c) = y;
+                    if (c == 0) a.slot_l[q] = l2;
+                } else if (a.part_o) {
+                    *reinterpret_cast<float4*>(a.part_o + (part * rows_all + at_y) * DIM + c) = y;
+                    if (c == 0) a.part_l[part * rows_all + at_y] = l2;
+                } else {
+                    *reinterpret_cast<uint2*>((bf16*)a.y + at_y * DIM + c) = make_uint2(rw_pack(y.x, y.y), rw_pack(y.z, y.w));
+                    if (a.lse && c == 0) a.lse[at_y] = l2 * 0.6931471805599453f;
+                }
+            }
+            __syncthreads();
         }
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        y.x *= inv; y.y *= inv; y.z *= inv; y.w *= inv;
-        const size_t at = row_at(a, n0, g, r).o;
-        const float l2 = sum == 0.f ? -INFINITY : ref + log2f(sum);
-        if (whole) {
-            *reinterpret_cast<uint2*>((bf16*)a.y + at * DIM + c) = make_uint2(rw_pack(y.x, y.y), rw_pack(y.z, y.w));
-            if (a.lse && c == 0) a.lse[at] = l2 * 0.6931471805599453f;
-        } else {
-            *reinterpret_cast<float4*>(a.part_o + (part * rows_all + at) * DIM + c) = y;
-            if (c == 0) a.part_l[part * rows_all + at] = l2;
-        }
+        clear();
+        first_group = false;
+        from = 0;
     }
+    umma::cp_async_wait<0>();
 }
 
-template <int DIM, int MT>
+template <int DIM>
 static cudaError_t launch_rows_t(const AttnArgs& a, cudaStream_t s) {
-    using Sh = RowsShape<DIM, MT>;
-    cudaError_t e = cudaFuncSetAttribute(attn_rows_kernel<DIM, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::BYTES);
+    using Sh = RowsShape<DIM>;
+    cudaError_t e = cudaFuncSetAttribute(attn_rows_kernel<DIM>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::BYTES);
     if (e != cudaSuccess) return e;
-    const unsigned grid = (a.by_shared == AttnBy::rows ? a.parts_shared * a.Hkv : 0) +
-                          (a.by_own == AttnBy::rows ? a.parts_own * a.Hkv * a.B : 0);
-    attn_rows_kernel<DIM, MT><<<grid, kRwWarps * 32, Sh::BYTES, s>>>(a);
+    const int per_head = a.even ? a.even : (a.by_shared == AttnBy::rows) + (a.by_own == AttnBy::rows ? a.B : 0);
+    attn_rows_kernel<DIM><<<(unsigned)per_head * a.Hkv, kRwWarps * 32, Sh::BYTES, s>>>(a);
     return cudaGetLastError();
 }
 
 cudaError_t launch_attn_rows(const AttnArgs& a, cudaStream_t s) {
-    const int rows = (a.by_shared == AttnBy::rows ? a.B : 1) * a.T * a.Gq;
-    if (a.d == 128) return rows <= 16 ? launch_rows_t<128, 1>(a, s) : launch_rows_t<128, 2>(a, s);
-    return rows <= 16 ? launch_rows_t<64, 1>(a, s) : launch_rows_t<64, 2>(a, s);
+    return a.d == 128 ? launch_rows_t<128>(a, s) : launch_rows_t<64>(a, s);
 }
 
 }  // namespace lola
