@@ -52,41 +52,56 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
             p1 = p0;
         }
     }
-    float m = -INFINITY;
-    for (int p = p0 + lane; p < p1; p += 32) m = fmaxf(m, a.part_l[p * rows + row]);
+    // A batch of 32 parts at a time: lane i looks up part i and its weight, then all lanes add its row.
+    const int np = p1 - p0, ns0 = c1[0] - c0[0] + 1, n = np + (ns0 > 0 ? ns0 : 0) + (c1[1] < 0 ? 0 : c1[1] - c0[1] + 1);
     auto slot = [&](int k, int c) {
         const bool second = c == c0[k] && (int)((long long)total * c / runs) != gb[k];     // not the group that CTA's run begins in
         return (size_t)(2 * (c * a.Hkv + g) + second) * a.slot_rows + rr[k];
     };
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-        for (int c = c0[k] + lane; c <= c1[k]; c += 32) m = fmaxf(m, a.slot_l[slot(k, c)]);
-    m = warp_max(m);
-    const float ref = m == -INFINITY ? 0.f : m;
-    float sum = 0.f, acc[EPL];
+    float m = -INFINITY, sum = 0.f, acc[EPL];
 #pragma unroll
     for (int u = 0; u < EPL; ++u) acc[u] = 0.f;
-    auto add = [&](const float* po, float pl) {
-        const float w = exp2f(pl - ref);
-        sum += w;
-        if (EPL == 4) {
-            const float4 x = *reinterpret_cast<const float4*>(po);
-            acc[0] = fmaf(w, x.x, acc[0]); acc[1] = fmaf(w, x.y, acc[1]);
-            acc[EPL - 2] = fmaf(w, x.z, acc[EPL - 2]); acc[EPL - 1] = fmaf(w, x.w, acc[EPL - 1]);
-        } else {
-            const float2 x = *reinterpret_cast<const float2*>(po);
-            acc[0] = fmaf(w, x.x, acc[0]); acc[1] = fmaf(w, x.y, acc[1]);
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        const int i = i0 + lane, cnt = min(32, n - i0);
+        const float* from = nullptr;
+        float l = -INFINITY;
+        if (i < np) {
+            const size_t q = (p0 + i) * rows + row;
+            from = a.part_o + q * DIM;
+            l = a.part_l[q];
+        } else if (i < n) {
+            const int k = i - np < ns0 ? 0 : 1;
+            const size_t q = slot(k, c0[k] + i - np - (k && ns0 > 0 ? ns0 : 0));
+            from = a.slot_o + q * DIM;
+            l = a.slot_l[q];
         }
-    };
-#pragma unroll 8
-    for (int p = p0; p < p1; ++p) add(a.part_o + (p * rows + row) * DIM + lane * EPL, a.part_l[p * rows + row]);
+        const float mn = fmaxf(m, warp_max(l)), ref = mn == -INFINITY ? 0.f : mn, f = exp2f(m - ref), w = exp2f(l - ref);
+        m = mn;
+        sum = sum * f + warp_sum(w);
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll 4
-        for (int c = c0[k]; c <= c1[k]; ++c) {
-            const size_t q = slot(k, c);
-            add(a.slot_o + q * DIM + lane * EPL, a.slot_l[q]);
+        for (int u = 0; u < EPL; ++u) acc[u] *= f;
+        for (int j0 = 0; j0 < cnt; j0 += 8) {
+            float x[8][EPL];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const unsigned long long po = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(from), j0 + j);
+                const float* row_p = reinterpret_cast<const float*>(po) + lane * EPL;
+#pragma unroll
+                for (int u = 0; u < EPL; ++u) x[j][u] = 0.f;
+                if (j0 + j < cnt) {
+                    if (EPL == 4) *reinterpret_cast<float4*>(x[j]) = *reinterpret_cast<const float4*>(row_p);
+                    else *reinterpret_cast<float2*>(x[j]) = *reinterpret_cast<const float2*>(row_p);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float wj = __shfl_sync(0xffffffffu, w, j0 + j);
+#pragma unroll
+                for (int u = 0; u < EPL; ++u) acc[u] = fmaf(wj, x[j][u], acc[u]);
+            }
         }
+    }
+    const float ref = m == -INFINITY ? 0.f : m;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
     for (int u = 0; u < EPL; ++u) store_as((TOut*)a.y + row * DIM + lane * EPL + u, acc[u] * inv);
@@ -210,11 +225,12 @@ cudaError_t launch_attn(const AttnArgs& a, int num_sms, int* launches, cudaStrea
         return x == cudaSuccess;
     };
     const bool f32 = a.dtype == 0;
-    auto by_tiles = [&](int packed) {
-        return f32 ? launch_attn_f32_tiles(a, packed, s) : launch_attn_tc(a, packed, num_sms, s);
-    };
-    if (a.by_shared == AttnBy::tiles && !run(by_tiles(1))) return e;
-    if (a.by_own == AttnBy::tiles && !run(by_tiles(0))) return e;
+    if (f32) {
+        if (a.by_shared == AttnBy::tiles && !run(launch_attn_f32_tiles(a, 1, s))) return e;
+        if (a.by_own == AttnBy::tiles && !run(launch_attn_f32_tiles(a, 0, s))) return e;
+    } else if ((a.by_shared == AttnBy::tiles || a.by_own == AttnBy::tiles) && !run(launch_attn_tc(a, num_sms, s))) {
+        return e;
+    }
     if ((a.by_shared == AttnBy::rows || a.by_own == AttnBy::rows) &&
         !run(f32 ? launch_attn_f32_rows(a, s) : launch_attn_rows(a, s)))
         return e;

@@ -60,9 +60,9 @@ cudaError_t launch_attn(const AttnArgs& a, int num_sms, int* launches, cudaStrea
 // bf16, up to kRowsMax rows per group (attn_rows.cu); the parts of both kinds that are its own
 constexpr int kRowsMax = 16;
 cudaError_t launch_attn_rows(const AttnArgs& a, cudaStream_t s);
-// bf16, any number of rows, 128 keys at a time (attn_tc.cu); packed: the shared keys' group
-cudaError_t launch_attn_tc(const AttnArgs& a, int packed, int num_sms, cudaStream_t s);
-// f32 (attn_f32.cu): up to kF32RowsMax rows of a sequence; any number of rows, packed as above
+// bf16, any number of rows, 128 keys at a time (attn_tc.cu); the parts of both kinds that are its own
+cudaError_t launch_attn_tc(const AttnArgs& a, int num_sms, cudaStream_t s);
+// f32 (attn_f32.cu): up to kF32RowsMax rows of a sequence; any number of rows, packed: the shared keys' group
 constexpr int kF32RowsMax = 16;
 cudaError_t launch_attn_f32_rows(const AttnArgs& a, cudaStream_t s);
 cudaError_t launch_attn_f32_tiles(const AttnArgs& a, int packed, cudaStream_t s);

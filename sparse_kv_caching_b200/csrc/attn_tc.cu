@@ -39,11 +39,11 @@ constexpr int kTcRows = 128, kTcKeys = 128, kTcThreads = 384;
 struct TcArgs {
     CUtensorMap map[4];             // shared keys and values, own keys and values
     AttnArgs a;
-    int packed;                     // 1: items are rows of the whole batch against the shared keys
-    int row_tiles;                  // 256-row tile pairs per group
-    int parts, chunk;               // key tiles per part
-    int part0;                      // first part's index in the workspace
-    int items;
+    // Two kinds of items: [0] rows of the whole batch against the shared keys, [1] rows of one sequence
+    // against its own keys, the shared ones first where they are walked.
+    int row_tiles[2];               // 256-row tile pairs per group
+    int parts[2], chunk[2];         // parts of a row, key tiles per part
+    int shared_items, items;        // the items of kind 0, of both
     int mh[4], mb[4];               // coordinate multipliers of the maps: 0 where one head (sequence) serves all
 };
 
@@ -109,30 +109,33 @@ __device__ __forceinline__ bool tc_wait_warp(uint64_t* mbar, uint32_t parity, vo
 
 // One work item: up to 256 rows of a group against a range of key tiles.
 struct TcItem {
-    int g, b, n0, R, r0, part;      // kv head, sequence, first token, rows of the group, first row, part
+    int g, b, n0, R, r0, part;      // kv head, sequence, first token, rows of the group, first row, part (in the workspace)
     int nt0, j0, j1, len;           // shared tiles of the walk, this part's tiles, own length
     bool two;                       // tile B holds rows
 };
 __device__ __forceinline__ TcItem tc_item(const TcArgs& p, int i) {
     const AttnArgs& a = p.a;
     TcItem x;
-    const int rt = i % p.row_tiles;
-    i /= p.row_tiles;
-    x.part = i % p.parts;
-    i /= p.parts;
+    const int own = i >= p.shared_items, row_tiles = p.row_tiles[own], parts = p.parts[own];
+    if (own) i -= p.shared_items;
+    const int rt = i % row_tiles;
+    i /= row_tiles;
+    const int k = i % parts;
+    i /= parts;
+    x.part = own ? a.parts_shared + k : k;
     x.g = i % a.Hkv;
-    x.b = i / a.Hkv;
+    x.b = i / a.Hkv;                // (0 for the shared keys)
     x.n0 = x.b * a.T;
-    x.R = (p.packed ? a.B : 1) * a.T * a.Gq;
+    x.R = (own ? 1 : a.B) * a.T * a.Gq;
     x.r0 = rt * 2 * kTcRows;
     const int last = min(x.R, x.r0 + 2 * kTcRows) - 1;
     x.two = last >= x.r0 + kTcRows;
-    x.len = p.packed ? 0 : own_length(a, x.b);
-    x.nt0 = p.packed || a.walk ? (a.shared.n + kTcKeys - 1) / kTcKeys : 0;
-    const int vis = p.packed ? 0 : own_visible(a, x.len, last / a.Gq);
+    x.len = own ? own_length(a, x.b) : 0;
+    x.nt0 = !own || a.walk ? (a.shared.n + kTcKeys - 1) / kTcKeys : 0;
+    const int vis = own ? own_visible(a, x.len, last / a.Gq) : 0;
     const int nt = x.nt0 + (vis + kTcKeys - 1) / kTcKeys;
-    x.j0 = min(nt, x.part * p.chunk);
-    x.j1 = min(nt, x.j0 + p.chunk);
+    x.j0 = min(nt, k * p.chunk[own]);
+    x.j1 = min(nt, x.j0 + p.chunk[own]);
     return x;
 }
 
@@ -443,7 +446,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             int Ro = row_ok ? R : 0;
             asm volatile("" : "+r"(Ro));
             const size_t at = row_at(a, x.n0, x.g, Ro).o;
-            const size_t po = (size_t)(p.part0 + x.part) * a.B * a.T * a.Hq + at;
+            const size_t po = (size_t)x.part * a.B * a.T * a.Hq + at;
             uint8_t* to = !row_ok ? nullptr
                           : a.part_o ? reinterpret_cast<uint8_t*>(a.part_o + po * DIM)
                                      : reinterpret_cast<uint8_t*>((bf16*)a.y + at * DIM);
@@ -547,23 +550,27 @@ cudaError_t launch_tc_t(const TcArgs& p, int num_sms, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_attn_tc(const AttnArgs& a, int packed, int num_sms, cudaStream_t s) {
+cudaError_t launch_attn_tc(const AttnArgs& a, int num_sms, cudaStream_t s) {
     TcArgs p{};
     const KeySeg &sh = a.shared, &ow = a.own;
-    if (sh.n > 0 && (packed || a.walk) && (!tc_map(p, 0, sh.k, a.d, sh.n, sh.ks, a.Hkv, sh.kh, 1, 0) ||
+    const bool shared = a.by_shared == AttnBy::tiles, own = a.by_own == AttnBy::tiles;
+    if (sh.n > 0 && (shared || a.walk) && (!tc_map(p, 0, sh.k, a.d, sh.n, sh.ks, a.Hkv, sh.kh, 1, 0) ||
                                            !tc_map(p, 1, sh.v, a.d, sh.n, sh.vs, a.Hkv, sh.vh, 1, 0)))
         return cudaErrorInvalidValue;
-    if (ow.n > 0 && !packed && (!tc_map(p, 2, ow.k, a.d, ow.n, ow.ks, a.Hkv, ow.kh, a.B, ow.kb) ||
-                                !tc_map(p, 3, ow.v, a.d, ow.n, ow.vs, a.Hkv, ow.vh, a.B, ow.vb)))
+    if (ow.n > 0 && own && (!tc_map(p, 2, ow.k, a.d, ow.n, ow.ks, a.Hkv, ow.kh, a.B, ow.kb) ||
+                            !tc_map(p, 3, ow.v, a.d, ow.n, ow.vs, a.Hkv, ow.vh, a.B, ow.vb)))
         return cudaErrorInvalidValue;
     p.a = a;
-    p.packed = packed;
-    const int rows = (packed ? a.B : 1) * a.T * a.Gq;
-    p.row_tiles = (rows + 2 * kTcRows - 1) / (2 * kTcRows);
-    p.parts = packed ? a.parts_shared : a.parts_own;
-    p.chunk = (packed ? a.chunk_shared : a.chunk_own) / kTcKeys;
-    p.part0 = packed ? 0 : a.parts_shared;
-    p.items = p.row_tiles * p.parts * a.Hkv * (packed ? 1 : a.B);
+    const int rows = a.T * a.Gq;
+    auto pairs = [](long long n) { return (int)((n + 2 * kTcRows - 1) / (2 * kTcRows)); };
+    p.row_tiles[0] = pairs((long long)a.B * rows);
+    p.row_tiles[1] = pairs(rows);
+    p.parts[0] = shared ? a.parts_shared : 1;
+    p.parts[1] = own ? a.parts_own : 1;
+    p.chunk[0] = a.chunk_shared / kTcKeys;
+    p.chunk[1] = a.chunk_own / kTcKeys;
+    p.shared_items = shared ? p.row_tiles[0] * p.parts[0] * a.Hkv : 0;
+    p.items = p.shared_items + (own ? p.row_tiles[1] * p.parts[1] * a.Hkv * a.B : 0);
     return a.d == 128 ? launch_tc_t<128>(p, num_sms, s) : launch_tc_t<64>(p, num_sms, s);
 }
 
