@@ -18,6 +18,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
     constexpr int EPL = DIM / 32;
     const size_t rows = (size_t)a.B * a.T * a.Hq, row = (size_t)blockIdx.x * 4 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
+    attn_wait_before();
     if (row >= rows) return;
     // parts in part_o: [p0, p1); of a group whose rounds were dealt evenly and that a cut goes through
     // (k = 0 shared, 1 own): the slots of CTAs c0 .. c1 instead
@@ -236,14 +237,9 @@ cudaError_t launch_attn(const AttnArgs& a, int num_sms, int* launches, cudaStrea
         return e;
     if (a.part_o || a.even) {
         const unsigned grid = (unsigned)(((size_t)a.B * a.T * a.Hq + 3) / 4);
-        if (f32) {
-            if (a.d == 128) attn_join_kernel<128, float><<<grid, 128, 0, s>>>(a);
-            else attn_join_kernel<64, float><<<grid, 128, 0, s>>>(a);
-        } else {
-            if (a.d == 128) attn_join_kernel<128, __nv_bfloat16><<<grid, 128, 0, s>>>(a);
-            else attn_join_kernel<64, __nv_bfloat16><<<grid, 128, 0, s>>>(a);
-        }
-        run(cudaGetLastError());
+        auto join = f32 ? (a.d == 128 ? attn_join_kernel<128, float> : attn_join_kernel<64, float>)
+                        : (a.d == 128 ? attn_join_kernel<128, __nv_bfloat16> : attn_join_kernel<64, __nv_bfloat16>);
+        run(attn_launch(join, grid, 128, 0, true, s, a));
     }
     return e;
 }

@@ -68,6 +68,28 @@ cudaError_t launch_attn_f32_rows(const AttnArgs& a, cudaStream_t s);
 cudaError_t launch_attn_f32_tiles(const AttnArgs& a, int packed, cudaStream_t s);
 cudaError_t attn_error_word(int* word, cudaStream_t s);
 
+// Programmatic dependent launch inside one call: a kernel launched `behind` another may begin before that one
+// has ended (its begin and first loads hide behind the other's end), and waits with attn_wait_before where it
+// needs what that one wrote.  The first kernel of a call is launched in plain stream order, so nothing of a call
+// begins before earlier work on the stream has ended.  attn_let_next_begin: the next kernel may be scheduled.
+__device__ __forceinline__ void attn_wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void attn_let_next_begin() { asm volatile("griddepcontrol.launch_dependents;"); }
+template <typename Args>
+cudaError_t attn_launch(void (*kernel)(const Args), unsigned grid, unsigned threads, size_t smem, bool behind, cudaStream_t s,
+                        const Args& args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = behind ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, args);
+}
+
 // Where row r of a group is: its token over the batch, its offset in q (elements), its index in y.
 struct RowAt {
     int n, t;

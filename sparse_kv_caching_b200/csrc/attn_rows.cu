@@ -91,6 +91,7 @@ __global__ void __launch_bounds__(kRwWarps * 32, 2) attn_rows_kernel(const __gri
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = blockIdx.x % a.Hkv, run = blockIdx.x / a.Hkv;
+    attn_let_next_begin();
 
     // ---- this CTA's run of rounds ----
     RowsAt at{};                                // where it begins
@@ -383,8 +384,7 @@ static cudaError_t launch_rows_t(const AttnArgs& a, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(attn_rows_kernel<DIM>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::BYTES);
     if (e != cudaSuccess) return e;
     const int per_head = a.even ? a.even : (a.by_shared == AttnBy::rows) + (a.by_own == AttnBy::rows ? a.B : 0);
-    attn_rows_kernel<DIM><<<(unsigned)per_head * a.Hkv, kRwWarps * 32, Sh::BYTES, s>>>(a);
-    return cudaGetLastError();
+    return attn_launch(attn_rows_kernel<DIM>, (unsigned)per_head * a.Hkv, kRwWarps * 32, Sh::BYTES, false, s, a);
 }
 
 cudaError_t launch_attn_rows(const AttnArgs& a, cudaStream_t s) {

@@ -154,6 +154,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Sh::FLAG);
     uint32_t* tptr = reinterpret_cast<uint32_t*>(smem + Sh::FLAG + 8);
 
+    attn_let_next_begin();
     if (warp == 0) umma::tmem_alloc(tptr, 512);
     if (tid == 0) {
         for (int i = 0; i < Sh::NBAR; ++i) umma::mbar_init(&mbar[i], 1);
