@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
 size_t plan_attn(AttnArgs& a, int num_sms) {
     a.walk = 1;
     a.by_shared = a.by_own = AttnBy::none;
-    a.parts_shared = a.parts_own = a.chunk_shared = a.chunk_own = a.even = a.slot_rows = 0;
+    a.parts_shared = a.parts_own = a.chunk_shared = a.chunk_own = a.even = a.slot_rows = a.beside = 0;
     const bool f32 = a.dtype == 0;
     const int rows = a.T * a.Gq, P = a.shared.n, L = a.own.n;
     const long long groups = (long long)a.B * a.Hkv, all_rows = (long long)a.B * rows;
@@ -178,10 +178,32 @@ size_t plan_attn(AttnArgs& a, int num_sms) {
         }
     }
     if (!f32 && (a.by_own == AttnBy::rows || a.by_shared == AttnBy::rows)) {
+        // The shared keys' tiles are bound by the tensor cores and by their own begin and end, the own keys
+        // by HBM, which a third of the SMs can keep busy: they run at the same time on SMs of their own, in
+        // the shares that end together.  In us: 1.9 for each pair of row tiles and key tile and 9 to begin
+        // and end; 0.09 MB per us and SM, 5 in all, and 4 to begin and end.
+        long long slots = 2LL * num_sms;
+        const long long base = tiles(all_rows, 256) * a.Hkv;
+        if (a.by_shared == AttnBy::tiles && a.by_own == AttnBy::rows && base + a.Hkv / 2 < num_sms) {
+            const long long key_tiles = tiles(P, 128);
+            const double mb = (double)groups * L * 4 * a.d * 1e-6;
+            double best = 1e30;
+            for (long long k = 1; base * k + a.Hkv / 2 < num_sms; ++k) {
+                const long long chunk = tiles(key_tiles, k), rest = num_sms - base * tiles(key_tiles, chunk);
+                const double t_own = 4 + mb / (0.09 * rest < 5 ? 0.09 * rest : 5), t_shared = 9 + 1.9 * chunk;
+                const double t = t_own > t_shared ? t_own : t_shared;
+                if (t < best) {
+                    best = t;
+                    a.parts_shared = (int)tiles(key_tiles, chunk);
+                    a.chunk_shared = (int)(chunk * 128);
+                    slots = 2 * rest;
+                }
+            }
+            a.beside = 1;
+        }
         // Rounds of 64 keys, a CTA per group or dealt evenly?  In rounds: a CTA on an SM of its own or with
         // one neighbour takes about one unit of time for each, and four for its begin and end; evenly
         // dealt work needs the join, about four more.
-        const long long slots = 2LL * num_sms;
         const long long sh = a.by_shared == AttnBy::rows ? tiles(P, kRwRound) : 0;
         const long long own = a.by_own == AttnBy::rows ? tiles((long long)n0 + L, kRwRound) : 0;
         const long long ctas = (sh ? a.Hkv : 0) + (own ? groups : 0), all = sh + own * a.B;      // of one head

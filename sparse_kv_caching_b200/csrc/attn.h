@@ -45,7 +45,7 @@ struct AttnArgs {
     float* part_l;         // [parts][B T Hq]
     // attn_rows_kernel with each kv head's rounds dealt evenly to this many CTAs (0: a CTA per group): what is
     // left of groups that a cut goes through, and the rounds before each sequence
-    int even, slot_rows;
+    int even, slot_rows, beside;       // beside: on SMs that the shared keys' tiles leave free, at the same time
     float* slot_o;         // [even][Hkv][2][slot_rows][d]
     float* slot_l;         // [even][Hkv][2][slot_rows]
     int* goff;             // [B + 1]
@@ -59,7 +59,7 @@ void place_attn(AttnArgs& a, void* workspace);       // sets the pointers into i
 cudaError_t launch_attn(const AttnArgs& a, int num_sms, int* launches, cudaStream_t s);
 // bf16, up to kRowsMax rows per group (attn_rows.cu); the parts of both kinds that are its own
 constexpr int kRowsMax = 16;
-cudaError_t launch_attn_rows(const AttnArgs& a, cudaStream_t s);
+cudaError_t launch_attn_rows(const AttnArgs& a, cudaStream_t s);   // (a.beside: behind launch_attn_tc)
 // bf16, any number of rows, 128 keys at a time (attn_tc.cu); the parts of both kinds that are its own
 cudaError_t launch_attn_tc(const AttnArgs& a, int num_sms, cudaStream_t s);
 // f32 (attn_f32.cu): up to kF32RowsMax rows of a sequence; any number of rows, packed: the shared keys' group

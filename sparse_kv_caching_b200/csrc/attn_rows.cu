@@ -150,7 +150,10 @@ __global__ void __launch_bounds__(kRwWarps * 32, 2) attn_rows_kernel(const __gri
         if (begin < sh_rounds) at = {1, 0, begin, sh_rounds};
         else at = {0, scan[8], scan[9], scan[10]};
     }
-    if (left == 0) return;
+    if (left == 0) {
+        if (a.beside) attn_wait_before();
+        return;
+    }
 
     // ---- copies, two rounds ahead of the products ----
     uint8_t* ring = smem + warp * Sh::WARP;
@@ -376,6 +379,9 @@ __global__ void __launch_bounds__(kRwWarps * 32, 2) attn_rows_kernel(const __gri
         from = 0;
     }
     umma::cp_async_wait<0>();
+    // The tile kernel that runs beside this one writes other parts: with this wait its end comes before this
+    // kernel's end, which is what the join waits for.
+    if (a.beside) attn_wait_before();
 }
 
 template <int DIM>
@@ -384,7 +390,7 @@ static cudaError_t launch_rows_t(const AttnArgs& a, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(attn_rows_kernel<DIM>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::BYTES);
     if (e != cudaSuccess) return e;
     const int per_head = a.even ? a.even : (a.by_shared == AttnBy::rows) + (a.by_own == AttnBy::rows ? a.B : 0);
-    return attn_launch(attn_rows_kernel<DIM>, (unsigned)per_head * a.Hkv, kRwWarps * 32, Sh::BYTES, false, s, a);
+    return attn_launch(attn_rows_kernel<DIM>, (unsigned)per_head * a.Hkv, kRwWarps * 32, Sh::BYTES, a.beside != 0, s, a);
 }
 
 cudaError_t launch_attn_rows(const AttnArgs& a, cudaStream_t s) {
