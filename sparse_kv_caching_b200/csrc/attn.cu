@@ -179,9 +179,9 @@ size_t plan_attn(AttnArgs& a, int num_sms) {
     }
     if (!f32 && (a.by_own == AttnBy::rows || a.by_shared == AttnBy::rows)) {
         // The shared keys' tiles are bound by the tensor cores and by their own begin and end, the own keys
-        // by HBM, which a third of the SMs can keep busy: they run at the same time on SMs of their own, in
-        // the shares that end together.  In us: 1.9 for each pair of row tiles and key tile and 9 to begin
-        // and end; 0.09 MB per us and SM, 5 in all, and 4 to begin and end.
+        // by HBM, or by how fast an SM turns them over: they run at the same time on SMs of their own, in
+        // the shares that end together.  Measured, in us: 1.75 for each pair of row tiles and key tile and 20
+        // for the rest; 0.04 MB per us and SM, 5.2 in all, and 5 for the rest.
         long long slots = 2LL * num_sms;
         const long long base = tiles(all_rows, 256) * a.Hkv;
         if (a.by_shared == AttnBy::tiles && a.by_own == AttnBy::rows && base + a.Hkv / 2 < num_sms) {
@@ -190,7 +190,7 @@ size_t plan_attn(AttnArgs& a, int num_sms) {
             double best = 1e30;
             for (long long k = 1; base * k + a.Hkv / 2 < num_sms; ++k) {
                 const long long chunk = tiles(key_tiles, k), rest = num_sms - base * tiles(key_tiles, chunk);
-                const double t_own = 4 + mb / (0.09 * rest < 5 ? 0.09 * rest : 5), t_shared = 9 + 1.9 * chunk;
+                const double t_own = 5 + mb / (0.04 * rest < 5.2 ? 0.04 * rest : 5.2), t_shared = 20 + 1.75 * chunk;
                 const double t = t_own > t_shared ? t_own : t_shared;
                 if (t < best) {
                     best = t;

@@ -10,16 +10,17 @@
 // once; each eighth of a warp has a softmax state of its own until the end.
 //
 // attn_f32_tile_kernel, many rows: bound by the multiply-adds (2 d per row and key
-// for each product).  64 rows x 32 keys per step, 4 rows x 2 keys of the scores and
+// for each product).  64 rows x 64 keys per step, 4 rows x 4 keys of the scores and
 // 4 rows x d / 16 columns of O per thread, operands from shared memory in 16-byte
-// words (K rows padded by one: no bank conflicts).
+// words (K rows padded by one: no bank conflicts); the next step's keys land meanwhile.
 #include "attn.h"
 #include "device_common.cuh"
+#include "umma.cuh"
 
 namespace lola {
 
 constexpr int kFrRows = 4, kFrThreads = 128, kFrUnroll = 2;
-constexpr int kFtRows = 64, kFtKeys = 32, kFtThreads = 256;
+constexpr int kFtRows = 64, kFtThreads = 256;
 
 // What a CTA reads: the group's rows and a range [lo, hi) of the walk, whose first np0 keys are shared.
 struct F32Work {
@@ -185,26 +186,26 @@ __global__ void __launch_bounds__(kFrThreads) attn_f32_rows_kernel(const __grid_
 
 template <int DIM>
 struct F32Tile {
-    static constexpr int LQ = DIM + 4, LP = kFtKeys + 4;
-    static constexpr int Q = 0, K = Q + kFtRows * LQ, V = K + kFtKeys * LQ, PP = V + kFtKeys * DIM,
-                         WORDS = PP + kFtRows * LP;
+    static constexpr int KEYS = 64, KPT = KEYS / 16;                   // keys of a step, and of a thread
+    static constexpr int LQ = DIM + 4, LP = KEYS + 4;
+    static constexpr int KV = KEYS * LQ + KEYS * DIM;                   // a stage: K (padded rows), then V
+    static constexpr int Q = 0, ST = Q + kFtRows * LQ, PP = ST + 2 * KV, WORDS = PP + kFtRows * LP;
 };
 
 template <int DIM>
-__global__ void __launch_bounds__(kFtThreads, 2) attn_f32_tile_kernel(const __grid_constant__ AttnArgs a, int packed) {
+__global__ void __launch_bounds__(kFtThreads) attn_f32_tile_kernel(const __grid_constant__ AttnArgs a, int packed) {
     using Sh = F32Tile<DIM>;
-    constexpr int NC = DIM / 64, LQ = Sh::LQ, LP = Sh::LP;
+    constexpr int NC = DIM / 64, LQ = Sh::LQ, LP = Sh::LP, KEYS = Sh::KEYS, KPT = Sh::KPT;
     extern __shared__ __align__(16) float fs[];
-    float *sq = fs + Sh::Q, *sk = fs + Sh::K, *sv = fs + Sh::V, *sp = fs + Sh::PP;
+    float *sq = fs + Sh::Q, *sp = fs + Sh::PP;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int row_tiles = ((packed ? a.B : 1) * a.T * a.Gq + kFtRows - 1) / kFtRows;
     const F32Work w = f32_work(a, blockIdx.x / row_tiles, packed);     // neighbours read the same keys
     const int r0 = (blockIdx.x % row_tiles) * kFtRows;
     for (int i = tid; i < kFtRows * DIM / 4; i += kFtThreads) {
         const int r = i / (DIM / 4), c = i % (DIM / 4) * 4;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r0 + r < w.R) x = *reinterpret_cast<const float4*>((const float*)a.q + row_at(a, w.n0, w.g, r0 + r).q + c);
-        *reinterpret_cast<float4*>(sq + r * LQ + c) = x;
+        const bool ok = r0 + r < w.R;
+        umma::cp_async16_zfill(sq + r * LQ + c, (const float*)a.q + row_at(a, w.n0, w.g, ok ? r0 + r : 0).q + c, ok);
     }
     float m[4], l[4];
     float4 o[4][NC];
@@ -220,55 +221,70 @@ __global__ void __launch_bounds__(kFtThreads, 2) attn_f32_tile_kernel(const __gr
     }
     {   // the last row of the tile reads furthest
         const int r = min(w.R, r0 + kFtRows) - 1;
-        most = min(w.hi, w.np0 + own_visible(a, w.len, row_at(a, w.n0, w.g, r).t));
-        if (packed) most = w.hi;
+        most = packed ? w.hi : min(w.hi, w.np0 + own_visible(a, w.len, row_at(a, w.n0, w.g, r).t));
     }
-    for (int k0 = w.lo; k0 < most; k0 += kFtKeys) {
-        __syncthreads();
-        for (int i = tid; i < kFtKeys * DIM / 4; i += kFtThreads) {
-            const int r = i / (DIM / 4), c = i % (DIM / 4) * 4, key = k0 + r;
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-            if (key < w.hi) {
-                x = *reinterpret_cast<const float4*>(f32_key(a, w, key) + c);
-                y = *reinterpret_cast<const float4*>(f32_value(a, w, key) + c);
+    // the keys of a step while the one before is computed
+    auto fetch = [&](int k0, int stage) {
+        if (k0 < most) {
+            float *sk = fs + Sh::ST + stage * Sh::KV, *sv = sk + KEYS * LQ;
+            for (int i = tid; i < KEYS * DIM / 4; i += kFtThreads) {
+                const int r = i / (DIM / 4), c = i % (DIM / 4) * 4, key = k0 + r;
+                const bool ok = key < w.hi;
+                umma::cp_async16_zfill(sk + r * LQ + c, ok ? (const void*)(f32_key(a, w, key) + c) : a.q, ok);
+                umma::cp_async16_zfill(sv + r * DIM + c, ok ? (const void*)(f32_value(a, w, key) + c) : a.q, ok);
             }
-            *reinterpret_cast<float4*>(sk + r * LQ + c) = x;
-            *reinterpret_cast<float4*>(sv + r * DIM + c) = y;
         }
+        umma::cp_async_commit();
+    };
+    fetch(w.lo, 0);
+    int stage = 0;
+    for (int k0 = w.lo; k0 < most; k0 += KEYS, stage ^= 1) {
+        fetch(most - k0 > KEYS ? k0 + KEYS : most, stage ^ 1);
+        umma::cp_async_wait<1>();
         __syncthreads();
-        float s[4][2];
+        const float *sk = fs + Sh::ST + stage * Sh::KV, *sv = sk + KEYS * LQ;
+        float s[4][KPT];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[i][0] = s[i][1] = 0.f;
-#pragma unroll 8
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int k = 0; k < KPT; ++k) s[i][k] = 0.f;
+#pragma unroll 4
         for (int c = 0; c < DIM; c += 4) {
-            const float4 ka = *reinterpret_cast<const float4*>(sk + tx * LQ + c);
-            const float4 kb = *reinterpret_cast<const float4*>(sk + (tx + 16) * LQ + c);
+            float4 kk[KPT];
+#pragma unroll
+            for (int k = 0; k < KPT; ++k) kk[k] = *reinterpret_cast<const float4*>(sk + (tx + 16 * k) * LQ + c);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float4 x = *reinterpret_cast<const float4*>(sq + (4 * ty + i) * LQ + c);
-                s[i][0] = dot4(x, ka, s[i][0]);
-                s[i][1] = dot4(x, kb, s[i][1]);
+#pragma unroll
+                for (int k = 0; k < KPT; ++k) s[i][k] = dot4(x, kk[k], s[i][k]);
             }
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float x0 = k0 + tx < lim[i] ? s[i][0] * a.scale_log2 : -INFINITY;
-            const float x1 = k0 + tx + 16 < lim[i] ? s[i][1] * a.scale_log2 : -INFINITY;
-            float mx = fmaxf(x0, x1);
+            float mx = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < KPT; ++k) {
+                s[i][k] = k0 + tx + 16 * k < lim[i] ? s[i][k] * a.scale_log2 : -INFINITY;
+                mx = fmaxf(mx, s[i][k]);
+            }
 #pragma unroll
             for (int k = 1; k < 16; k <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
             const float mn = fmaxf(m[i], mx), ref = mn == -INFINITY ? 0.f : mn, f = exp2f(m[i] - ref);
-            const float p0 = exp2f(x0 - ref), p1 = exp2f(x1 - ref);
             m[i] = mn;
-            l[i] = l[i] * f + (p0 + p1);          // this thread's keys only: summed at the end
-            sp[(4 * ty + i) * LP + tx] = p0;
-            sp[(4 * ty + i) * LP + tx + 16] = p1;
+            l[i] *= f;                            // this thread's keys only: summed at the end
+#pragma unroll
+            for (int k = 0; k < KPT; ++k) {
+                const float p = exp2f(s[i][k] - ref);
+                l[i] += p;
+                sp[(4 * ty + i) * LP + tx + 16 * k] = p;
+            }
 #pragma unroll
             for (int j = 0; j < NC; ++j) { o[i][j].x *= f; o[i][j].y *= f; o[i][j].z *= f; o[i][j].w *= f; }
         }
         __syncwarp();                             // a row's weights are written and read by one warp
 #pragma unroll 2
-        for (int k = 0; k < kFtKeys; k += 4) {
+        for (int k = 0; k < KEYS; k += 4) {
             float4 p[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4*>(sp + (4 * ty + i) * LP + k);
@@ -285,7 +301,9 @@ __global__ void __launch_bounds__(kFtThreads, 2) attn_f32_tile_kernel(const __gr
                     }
                 }
         }
+        __syncthreads();                          // the stage is free
     }
+    umma::cp_async_wait<0>();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
 #pragma unroll

@@ -184,19 +184,32 @@ __global__ void __launch_bounds__(kRwWarps * 32, 2) attn_rows_kernel(const __gri
             uint8_t* st = ring + stage_in * Sh::STAGE;
             const int k0 = ahead.round * kRwRound + warp * kRwKeys;
             constexpr int RPI = 32 / KC;        // rows per pass
-#pragma unroll
-            for (int it = 0; it < kRwKeys / RPI; ++it) {
-                const int r = it * RPI + lane / KC, c = lane % KC, key = k0 + r;
-                const bool ok = key < n_keys;
-                const bf16* kp = fk + (key - np0) * fks;
-                const bf16* vp = fv + (key - np0) * fvs;
-                if (key < np0) {
-                    kp = sk + key * a.shared.ks;
-                    vp = sv + key * a.shared.vs;
-                }
+            const int c = lane % KC;
+            auto copy = [&](int r, const bf16* kp, const bf16* vp, bool ok) {
                 const uint32_t off = r * RB + ((c ^ (r & 7)) << 4);
                 umma::cp_async16_zfill(st + off, ok ? (const void*)kp : a.q, ok);
                 umma::cp_async16_zfill(st + kRwKeys * RB + off, ok ? (const void*)vp : a.q, ok);
+            };
+            if (k0 >= np0 || k0 + kRwKeys <= np0) {       // all own (or the shared group's), or all shared
+                const bool front = k0 < np0;
+                const long long ks = front ? a.shared.ks : fks, vs = front ? a.shared.vs : fvs;
+                const int key = k0 + lane / KC;
+                const bf16* kp = (front ? sk : fk) + (key - (front ? 0 : np0)) * ks;
+                const bf16* vp = (front ? sv : fv) + (key - (front ? 0 : np0)) * vs;
+#pragma unroll
+                for (int it = 0; it < kRwKeys / RPI; ++it) {
+                    copy(it * RPI + lane / KC, kp, vp, key + it * RPI < n_keys);
+                    kp += RPI * ks;
+                    vp += RPI * vs;
+                }
+            } else {
+#pragma unroll 1
+                for (int it = 0; it < kRwKeys / RPI; ++it) {
+                    const int r = it * RPI + lane / KC, key = k0 + r;
+                    const bool front = key < np0;
+                    copy(r, front ? sk + key * a.shared.ks : fk + (key - np0) * fks,
+                         front ? sv + key * a.shared.vs : fv + (key - np0) * fvs, key < n_keys);
+                }
             }
             stage_in = stage_in + 1 == kRwStages ? 0 : stage_in + 1;
             const bool last = ahead.round + 1 == ahead.rounds;
@@ -255,16 +268,25 @@ __global__ void __launch_bounds__(kRwWarps * 32, 2) attn_rows_kernel(const __gri
         const uint32_t ks = ring_s + stage * Sh::STAGE, vs = ks + kRwKeys * RB;
         stage = stage + 1 == kRwStages ? 0 : stage + 1;
         const int k0 = at.round * kRwRound + warp * kRwKeys;
+        // (loads of four steps in front of their products, two accumulators for each 8 keys: the warp has one
+        // neighbour on its scheduler at most, so latencies show)
+        float s2[2][2][4];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s2[i >> 3][i >> 2 & 1][i & 3] = 0.f;
+#pragma unroll
+        for (int k4 = 0; k4 < DIM / 16; k4 += 4) {
+            uint32_t kf[4][4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) rw_ldsm(kf[k], ks + krow * RB + (((2 * (k4 + k) + kch) ^ (krow & 7)) << 4));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                rw_mma(s2[k & 1][0], qf[k4 + k], kf[k][0], kf[k][1]);
+                rw_mma(s2[k & 1][1], qf[k4 + k], kf[k][2], kf[k][3]);
+            }
+        }
         float s[2][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[0][i] = s[1][i] = 0.f;
-#pragma unroll
-        for (int kk = 0; kk < DIM / 16; ++kk) {
-            uint32_t kf[4];
-            rw_ldsm(kf, ks + krow * RB + (((2 * kk + kch) ^ (krow & 7)) << 4));
-            rw_mma(s[0], qf[kk], kf[0], kf[1]);
-            rw_mma(s[1], qf[kk], kf[2], kf[3]);
-        }
+        for (int i = 0; i < 8; ++i) s[i >> 2][i & 3] = s2[0][i >> 2][i & 3] + s2[1][i >> 2][i & 3];
         uint32_t ph[4], pl[4];
         float f[2];
         bool up = false;
@@ -301,13 +323,17 @@ __global__ void __launch_bounds__(kRwWarps * 32, 2) attn_rows_kernel(const __gri
                 for (int i = 0; i < 4; ++i) o[n][i] *= f[i >> 1];
         }
 #pragma unroll
-        for (int n2 = 0; n2 < DIM / 16; ++n2) {
-            uint32_t vf[4];
-            rw_ldsm_t(vf, vs + vrow * RB + (((2 * n2 + vch) ^ (vrow & 7)) << 4));
-            rw_mma(o[2 * n2], ph, vf[0], vf[1]);
-            rw_mma(o[2 * n2 + 1], ph, vf[2], vf[3]);
-            rw_mma(o[2 * n2], pl, vf[0], vf[1]);
-            rw_mma(o[2 * n2 + 1], pl, vf[2], vf[3]);
+        for (int n4 = 0; n4 < DIM / 16; n4 += 4) {
+            uint32_t vf[4][4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) rw_ldsm_t(vf[n], vs + vrow * RB + (((2 * (n4 + n) + vch) ^ (vrow & 7)) << 4));
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    rw_mma(o[2 * (n4 + n)], h ? pl : ph, vf[n][0], vf[n][1]);
+                    rw_mma(o[2 * (n4 + n) + 1], h ? pl : ph, vf[n][2], vf[n][3]);
+                }
         }
         const bool group_ends = at.round + 1 == at.rounds;
         if (!group_ends && left > 1) {
