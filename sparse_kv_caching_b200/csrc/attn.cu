@@ -127,11 +127,11 @@ size_t plan_attn(AttnArgs& a, int num_sms) {
         if (*chunk == 0) *chunk = unit;
         *parts = n > 0 ? (int)tiles(n, *chunk) : 1;
     };
-    // f32: two CTAs per SM, parts of at least 128 keys; bf16 tiles: one per SM, four tiles of 128 keys.
+    // f32: parts of at least 128 keys, four CTAs per SM (two at a time: ragged lengths even out); bf16 tiles: one per SM, four tiles of 128 keys.
     auto cut_tiles = [&](long long n0, long long n1, long long r, long long heads, int* parts, int* chunk) {
         long long c;
         if (f32) {
-            cut(n0 + n1, tiles(r, 64) * heads, 2LL * num_sms, 32, 128, parts, &c);
+            cut(n0 + n1, tiles(r, 64) * heads, 4LL * num_sms, 64, 128, parts, &c);
             *chunk = (int)c;
         } else {
             cut(tiles(n0, 128) + tiles(n1, 128), tiles(r, 256) * heads, num_sms, 1, 4, parts, &c);

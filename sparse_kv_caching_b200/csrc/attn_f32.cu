@@ -10,7 +10,7 @@
 // once; each eighth of a warp has a softmax state of its own until the end.
 //
 // attn_f32_tile_kernel, many rows: bound by the multiply-adds (2 d per row and key
-// for each product).  64 rows x 64 keys per step, 4 rows x 4 keys of the scores and
+// for each product).  64 rows x 64 keys (d = 128: 32) per step, 4 rows x 4 keys (2) of the scores and
 // 4 rows x d / 16 columns of O per thread, operands from shared memory in 16-byte
 // words (K rows padded by one: no bank conflicts); the next step's keys land meanwhile.
 #include "attn.h"
@@ -186,14 +186,14 @@ __global__ void __launch_bounds__(kFrThreads) attn_f32_rows_kernel(const __grid_
 
 template <int DIM>
 struct F32Tile {
-    static constexpr int KEYS = 64, KPT = KEYS / 16;                   // keys of a step, and of a thread
+    static constexpr int KEYS = DIM == 64 ? 64 : 32, KPT = KEYS / 16;   // keys of a step (two CTAs share an SM), of a thread
     static constexpr int LQ = DIM + 4, LP = KEYS + 4;
     static constexpr int KV = KEYS * LQ + KEYS * DIM;                   // a stage: K (padded rows), then V
     static constexpr int Q = 0, ST = Q + kFtRows * LQ, PP = ST + 2 * KV, WORDS = PP + kFtRows * LP;
 };
 
 template <int DIM>
-__global__ void __launch_bounds__(kFtThreads) attn_f32_tile_kernel(const __grid_constant__ AttnArgs a, int packed) {
+__global__ void __launch_bounds__(kFtThreads, 2) attn_f32_tile_kernel(const __grid_constant__ AttnArgs a, int packed) {
     using Sh = F32Tile<DIM>;
     constexpr int NC = DIM / 64, LQ = Sh::LQ, LP = Sh::LP, KEYS = Sh::KEYS, KPT = Sh::KPT;
     extern __shared__ __align__(16) float fs[];
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(kFtThreads) attn_f32_tile_kernel(const __grid_
         umma::cp_async16_zfill(sq + r * LQ + c, (const float*)a.q + row_at(a, w.n0, w.g, ok ? r0 + r : 0).q + c, ok);
     }
     float m[4], l[4];
-    float4 o[4][NC];
+    ulonglong2 o[4][NC];                          // four columns each, in pairs
     int lim[4], most = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kFtThreads) attn_f32_tile_kernel(const __grid_
         m[i] = -INFINITY;
         l[i] = 0.f;
 #pragma unroll
-        for (int j = 0; j < NC; ++j) o[i][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int j = 0; j < NC; ++j) o[i][j] = make_ulonglong2(0ull, 0ull);
     }
     {   // the last row of the tile reads furthest
         const int r = min(w.R, r0 + kFtRows) - 1;
@@ -243,23 +243,33 @@ __global__ void __launch_bounds__(kFtThreads) attn_f32_tile_kernel(const __grid_
         umma::cp_async_wait<1>();
         __syncthreads();
         const float *sk = fs + Sh::ST + stage * Sh::KV, *sv = sk + KEYS * LQ;
+        // (pairs of multiply-adds: even dims in the low halves, odd ones in the high)
+        unsigned long long s2[4][KPT];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int k = 0; k < KPT; ++k) s2[i][k] = 0ull;
+#pragma unroll 4
+        for (int c = 0; c < DIM; c += 4) {
+            ulonglong2 kk[KPT];
+#pragma unroll
+            for (int k = 0; k < KPT; ++k) kk[k] = *reinterpret_cast<const ulonglong2*>(sk + (tx + 16 * k) * LQ + c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(sq + (4 * ty + i) * LQ + c);
+#pragma unroll
+                for (int k = 0; k < KPT; ++k) s2[i][k] = f2fma(x.y, kk[k].y, f2fma(x.x, kk[k].x, s2[i][k]));
+            }
+        }
         float s[4][KPT];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int k = 0; k < KPT; ++k) s[i][k] = 0.f;
-#pragma unroll 4
-        for (int c = 0; c < DIM; c += 4) {
-            float4 kk[KPT];
-#pragma unroll
-            for (int k = 0; k < KPT; ++k) kk[k] = *reinterpret_cast<const float4*>(sk + (tx + 16 * k) * LQ + c);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float4 x = *reinterpret_cast<const float4*>(sq + (4 * ty + i) * LQ + c);
-#pragma unroll
-                for (int k = 0; k < KPT; ++k) s[i][k] = dot4(x, kk[k], s[i][k]);
+            for (int k = 0; k < KPT; ++k) {
+                float lo, hi;
+                f2unpack(s2[i][k], lo, hi);
+                s[i][k] = lo + hi;
             }
-        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float mx = -INFINITY;
@@ -280,7 +290,10 @@ __global__ void __launch_bounds__(kFtThreads) attn_f32_tile_kernel(const __grid_
                 sp[(4 * ty + i) * LP + tx + 16 * k] = p;
             }
 #pragma unroll
-            for (int j = 0; j < NC; ++j) { o[i][j].x *= f; o[i][j].y *= f; o[i][j].z *= f; o[i][j].w *= f; }
+            for (int j = 0; j < NC; ++j) {
+                o[i][j].x = f2fma(o[i][j].x, f2pack(f, f), 0ull);
+                o[i][j].y = f2fma(o[i][j].y, f2pack(f, f), 0ull);
+            }
         }
         __syncwarp();                             // a row's weights are written and read by one warp
 #pragma unroll 2
@@ -292,12 +305,12 @@ __global__ void __launch_bounds__(kFtThreads) attn_f32_tile_kernel(const __grid_
             for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
                 for (int j = 0; j < NC; ++j) {
-                    const float4 x = *reinterpret_cast<const float4*>(sv + (k + kk) * DIM + 64 * j + 4 * tx);
+                    const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(sv + (k + kk) * DIM + 64 * j + 4 * tx);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float y = kk == 0 ? p[i].x : kk == 1 ? p[i].y : kk == 2 ? p[i].z : p[i].w;
-                        o[i][j].x = fmaf(y, x.x, o[i][j].x); o[i][j].y = fmaf(y, x.y, o[i][j].y);
-                        o[i][j].z = fmaf(y, x.z, o[i][j].z); o[i][j].w = fmaf(y, x.w, o[i][j].w);
+                        o[i][j].x = f2fma(f2pack(y, y), x.x, o[i][j].x);
+                        o[i][j].y = f2fma(f2pack(y, y), x.y, o[i][j].y);
                     }
                 }
         }
@@ -312,7 +325,12 @@ __global__ void __launch_bounds__(kFtThreads) attn_f32_tile_kernel(const __grid_
         if (r >= w.R) continue;
         const size_t at = row_at(a, w.n0, w.g, r).o;
 #pragma unroll
-        for (int j = 0; j < NC; ++j) f32_store(a, w, at, 64 * j + 4 * tx, o[i][j], m[i], l[i]);
+        for (int j = 0; j < NC; ++j) {
+            float4 y;
+            f2unpack(o[i][j].x, y.x, y.y);
+            f2unpack(o[i][j].y, y.z, y.w);
+            f32_store(a, w, at, 64 * j + 4 * tx, y, m[i], l[i]);
+        }
     }
 }
 
