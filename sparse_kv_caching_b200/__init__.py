@@ -250,15 +250,8 @@ def _attn_call(cfg, need, q, kp, vp, k, v, lens, y, lse, workspace):
 
 def attention_workspace(q, k, k_prefix=None) -> int:
     """Bytes of scratch that cross_attention(q, k, ...) or prefix_attention(q, k_prefix, ..., k, ...) uses."""
-    c = LolaAttnConfig(q.shape[0], q.shape[1], q.shape[2], k.shape[2], q.shape[3], _DTYPE_CODE[q.dtype],
-                       0 if k_prefix is None else k_prefix.shape[0], k.shape[1], 1.0)
-    unit = 16 // q.element_size()                    # (strides do not matter here)
-    for f in ("q_stride", "kp_stride", "vp_stride", "k_stride", "v_stride"):
-        for i in range(len(getattr(c, f))):
-            getattr(c, f)[i] = unit
-    n = c_size_t()
-    _check(lib().lola_attn_workspace(byref(c), byref(n)))
-    return n.value
+    pre = (None, None) if k_prefix is None else (k_prefix.shape, k_prefix.stride())
+    return _attn_plan(q.shape, k.shape, pre[0], q.stride(), k.stride(), k.stride(), pre[1], pre[1], q.dtype, 1.0)[1]
 
 
 def attention_check(stream=None) -> None:
