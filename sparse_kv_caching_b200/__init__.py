@@ -231,11 +231,11 @@ def _attention(q, kp, vp, k, v, lens, lens_name, scale, y, lse, workspace, strea
 
 
 def _attn_call(cfg, need, q, kp, vp, k, v, lens, y, lse, workspace):
-    if y is None:
-        y = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if y is None:                                     # (empty_like is the quickest, but keeps q's strides)
+        y = torch.empty_like(q) if q.is_contiguous() else q.new_empty(q.shape)
     if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    ws, size = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+        workspace = q.new_empty(-(-need // q.element_size()))
+    ws, size = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
     n, ls = 0 if lens is None else lens.data_ptr(), 0 if lse is None else lse.data_ptr()
     st = torch.cuda.current_stream(q.device.index).cuda_stream      # (without an index it is looked up, slowly)
     if kp is None:

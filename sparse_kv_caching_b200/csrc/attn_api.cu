@@ -63,14 +63,21 @@ lola::AttnArgs make_args(const lola_attn_config* c, int causal) {
     return a;
 }
 
-// SMs of the current device; without one (size queries on a host without a GPU) those of a B200.
+// SMs of the current device (asked of the driver once); without a device (size queries on a host that
+// has none) those of a B200.
 int sm_count() {
+    static std::atomic<int> known[64];
     int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    if (cudaGetDevice(&dev) != cudaSuccess) {
         (void)cudaGetLastError();
         return 148;
     }
+    if (dev < 64 && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return 148;
+    }
+    if (dev < 64) known[dev].store(sms, std::memory_order_relaxed);
     return sms;
 }
 
