@@ -13,6 +13,8 @@
 // for each product).  64 rows x 64 keys (d = 128: 32) per step, 4 rows x 4 keys (2) of the scores and
 // 4 rows x d / 16 columns of O per thread, operands from shared memory in 16-byte
 // words (K rows padded by one: no bank conflicts); the next step's keys land meanwhile.
+// B200: 2 x 333 queries x 1001 states, 12/4 heads, d 64: 68 us, 23 TFLOP/s with the join; the
+// rows kernel, 7 tokens after 4095 shared keys, 6/2 heads, d 64: 12 us.
 #include "attn.h"
 #include "device_common.cuh"
 #include "umma.cuh"

@@ -21,6 +21,8 @@
 // whole; what a CTA has of a group that a cut goes through is left in one of its two slots
 // (the group its run begins in, the one it ends in), and attn_join_kernel puts the
 // slots together.
+// B200, one token of 64 sequences against 1500 states, 32/8 heads, d 128: 64.9 us for 393 MB,
+// 6.07 TB/s (93 % of a copy); a CTA per group took 70 us for ragged lengths, dealt evenly 56.
 #include "attn.h"
 #include "umma.cuh"
 
