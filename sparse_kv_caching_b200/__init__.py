@@ -154,69 +154,81 @@ def _stream(stream=None) -> c_void_p:
 
 
 # -- exact attention beside the layer ---------------------------------------------
+# The current stream's handle by device index, without the wrapper object (1 us less a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _what(x):
+    """What a call's checks and plan depend on: equal for equal shapes, strides, dtypes and devices."""
+    return x.shape, x.stride(), x.dtype, x.device
+
+
+def _attn_same(got, name, shape, dtype, device, packed=False):
+    if got[0] != shape:
+        raise ValueError(f"{name}: shape {tuple(got[0])}, expected {tuple(shape)}")
+    if got[2] != dtype:
+        raise ValueError(f"{name}: dtype {got[2]}, expected {dtype}")
+    if got[3] != device:
+        raise ValueError(f"{name}: on {got[3]}, expected {device}")
+    if packed:
+        want = 1
+        for n, st in zip(reversed(got[0]), reversed(got[1])):
+            if n > 1 and st != want:
+                raise ValueError(f"{name} must be contiguous")
+            want *= n
+
+
 @functools.lru_cache(maxsize=4096)
-def _attn_plan(qs, ks, ps, q_st, k_st, v_st, kp_st, vp_st, dtype, scale):
-    """(config, bytes of workspace) of a call, from its shapes and strides alone."""
+def _attn_plan(q, k, v, kp, vp, lens, lens_name, y, lse, scale):
+    """(config, bytes of workspace) of a call, from what its tensors are (see _what) alone."""
+    qs, q_st, dtype, dev = q
+    ks, k_st = k[:2]
+    if dev.type != "cuda":
+        raise ValueError(f"q: on {dev}, expected a CUDA device")
     if dtype not in _DTYPE_CODE:
         raise ValueError(f"q: dtype {dtype}, expected one of {list(_DTYPE_CODE)}")
     if len(qs) != 4 or len(ks) != 4:
         raise ValueError(f"q and k must have 4 dimensions: shapes {tuple(qs)}, {tuple(ks)}")
     B, T, Hq, d = qs
     L, Hkv = ks[1], ks[2]
-    if tuple(ks) != (B, L, Hkv, d):
-        raise ValueError(f"k: shape {tuple(ks)}, expected {(B, L, Hkv, d)}")
+    _attn_same(k, "k", (B, L, Hkv, d), dtype, dev)
+    _attn_same(v, "v", ks, dtype, dev)
     P = 0
-    if ps is not None:
-        if len(ps) != 3 or tuple(ps[1:]) != (Hkv, d):
-            raise ValueError(f"k_prefix: shape {tuple(ps)}, expected (P, {Hkv}, {d})")
-        P = ps[0]
-    for st, name, n in ((q_st, "q", B * T * Hq), (k_st, "k", L), (v_st, "v", L), (kp_st, "k_prefix", P), (vp_st, "v_prefix", P)):
-        if n and st[-1] != 1:
+    if kp is not None:
+        if len(kp[0]) != 3:
+            raise ValueError(f"k_prefix must have 3 dimensions: shape {tuple(kp[0])}")
+        P = kp[0][0]
+        _attn_same(kp, "k_prefix", (P, Hkv, d), dtype, dev)
+        _attn_same(vp, "v_prefix", kp[0], dtype, dev)
+    if lens is not None:
+        _attn_same(lens, lens_name, (B,), torch.int32, dev, packed=True)
+    if y is not None:
+        _attn_same(y, "y", qs, dtype, dev, packed=True)
+    if lse is not None:
+        _attn_same(lse, "lse", qs[:3], torch.float32, dev, packed=True)
+    for x, name, n in ((q, "q", B * T * Hq), (k, "k", L), (v, "v", L), (kp, "k_prefix", P), (vp, "v_prefix", P)):
+        if n and x[1][-1] != 1:
             raise ValueError(f"{name}: the head's elements must be contiguous (last stride 1)")
     c = LolaAttnConfig(B, T, Hq, Hkv, d, _DTYPE_CODE[dtype], P, L, d ** -0.5 if scale is None else scale, q_st[:3],
-                       kp_st[:2] if P else (0, 0), vp_st[:2] if P else (0, 0), k_st[:3], v_st[:3])
+                       kp[1][:2] if P else (0, 0), vp[1][:2] if P else (0, 0), k_st[:3], v[1][:3])
     n = c_size_t()
     _check(lib().lola_attn_workspace(byref(c), byref(n)))
     return c, n.value
 
 
-def _attn_same(x, name, shape, dtype, device, packed=False):
-    if not isinstance(x, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if x.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(x.shape)}, expected {tuple(shape)}")
-    if x.dtype != dtype:
-        raise ValueError(f"{name}: dtype {x.dtype}, expected {dtype}")
-    if x.device != device:
-        raise ValueError(f"{name}: on {x.device}, expected {device}")
-    if packed and not x.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-
-
 def _attention(q, kp, vp, k, v, lens, lens_name, scale, y, lse, workspace, stream):
-    for x, name in ((q, "q"), (k, "k"), (v, "v")):
-        if not isinstance(x, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-    dev, dt, qs, ks = q.device, q.dtype, q.shape, k.shape
-    if dev.type != "cuda":
-        raise ValueError(f"q: on {dev}, expected a CUDA device")
-    _attn_same(k, "k", ks, dt, dev)
-    _attn_same(v, "v", ks, dt, dev)
-    ps = kp_st = vp_st = None
-    if kp is not None:
-        if not isinstance(kp, torch.Tensor):
-            raise TypeError("k_prefix must be a torch.Tensor")
-        ps, kp_st = kp.shape, kp.stride()
-        _attn_same(kp, "k_prefix", ps, dt, dev)
-        _attn_same(vp, "v_prefix", ps, dt, dev)
-        vp_st = vp.stride()
-    cfg, need = _attn_plan(qs, ks, ps, q.stride(), k.stride(), v.stride(), kp_st, vp_st, dt, scale)
-    if lens is not None:
-        _attn_same(lens, lens_name, qs[:1], torch.int32, dev, packed=True)
-    if y is not None:
-        _attn_same(y, "y", qs, dt, dev, packed=True)
-    if lse is not None:
-        _attn_same(lse, "lse", qs[:3], torch.float32, dev, packed=True)
+    try:
+        cfg, need = _attn_plan(_what(q), _what(k), _what(v), None if kp is None else _what(kp),
+                               None if vp is None else _what(vp), None if lens is None else _what(lens), lens_name,
+                               None if y is None else _what(y), None if lse is None else _what(lse), scale)
+    except AttributeError:
+        for x, name in ((q, "q"), (k, "k"), (v, "v"), (kp, "k_prefix"), (vp, "v_prefix"), (lens, lens_name), (y, "y"),
+                        (lse, "lse")):
+            if not isinstance(x, torch.Tensor) and (x is not None or name in ("q", "k", "v")):
+                raise TypeError(f"{name} must be a torch.Tensor") from None
+        raise
+    dev = q.device
     if workspace is not None and not (isinstance(workspace, torch.Tensor) and workspace.dtype == torch.uint8
                                       and workspace.device == dev and workspace.is_contiguous()):
         raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
@@ -237,21 +249,22 @@ def _attn_call(cfg, need, q, kp, vp, k, v, lens, y, lse, workspace):
         workspace = q.new_empty(-(-need // q.element_size()))
     ws, size = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
     n, ls = 0 if lens is None else lens.data_ptr(), 0 if lse is None else lse.data_ptr()
-    st = torch.cuda.current_stream(q.device.index).cuda_stream      # (without an index it is looked up, slowly)
+    st = _raw_stream(q.device.index)
     if kp is None:
         rc = _lib.lola_cross_attention(byref(cfg), q.data_ptr(), k.data_ptr(), v.data_ptr(), n, y.data_ptr(), ls, ws,
                                        size, st)
     else:
         rc = _lib.lola_prefix_attention(byref(cfg), q.data_ptr(), kp.data_ptr(), vp.data_ptr(), k.data_ptr(),
                                         v.data_ptr(), n, y.data_ptr(), ls, ws, size, st)
-    _check(rc)
+    if rc:
+        _check(rc)
     return y
 
 
 def attention_workspace(q, k, k_prefix=None) -> int:
     """Bytes of scratch that cross_attention(q, k, ...) or prefix_attention(q, k_prefix, ..., k, ...) uses."""
-    pre = (None, None) if k_prefix is None else (k_prefix.shape, k_prefix.stride())
-    return _attn_plan(q.shape, k.shape, pre[0], q.stride(), k.stride(), k.stride(), pre[1], pre[1], q.dtype, 1.0)[1]
+    pre = None if k_prefix is None else _what(k_prefix)
+    return _attn_plan(_what(q), _what(k), _what(k), pre, pre, None, "", None, None, 1.0)[1]
 
 
 def attention_check(stream=None) -> None:
