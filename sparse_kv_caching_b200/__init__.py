@@ -148,17 +148,16 @@ def prefill_once_noalloc(cfg: LolaConfig, W, q, k, v, y, stream=None):
     return y
 
 
-def _stream(stream=None) -> c_void_p:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return c_void_p(s.cuda_stream)
-
-
-# -- exact attention beside the layer ---------------------------------------------
 # The current stream's handle by device index, without the wrapper object (1 us less a call).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+def _stream(stream=None) -> c_void_p:
+    return c_void_p(_raw_stream(torch.cuda.current_device()) if stream is None else stream.cuda_stream)
+
+
+# -- exact attention beside the layer ---------------------------------------------
 def _what(x):
     """What a call's checks and plan depend on: equal for equal shapes, strides, dtypes and devices."""
     return x.shape, x.stride(), x.dtype, x.device
