@@ -171,8 +171,10 @@ size_t plan_attn(AttnArgs& a, int num_sms) {
             a.by_own = AttnBy::rows;
             a.parts_own = 1;
             if (f32) {
+                // (two CTAs per SM: with four the join of twice the parts costs more than the shorter walks
+                // save, 20 against 15 us for 7 tokens after 4095 shared keys)
                 long long c;
-                cut((long long)n0 + L, groups * tiles(rows, 4), 2LL * num_sms, 32, 128, &a.parts_own, &c);
+                cut((long long)n0 + L, groups * tiles(rows, 4), 2LL * num_sms, 32, 64, &a.parts_own, &c);
                 a.chunk_own = (int)c;
             }
         }
