@@ -80,7 +80,8 @@ typedef struct lola_config {
 
 typedef struct lola_state lola_state;   /* opaque host handle */
 
-/* Device views of the state (for checks and checkpoints).  Slot layouts:
+/* Device views of the state (for checks and checkpoints; B is the number of
+ * sequences that calls process, see lola_set_batch).  Slot layouts:
  *   H [B*Hkv][D][d] f32, s [B*Hkv][D] f32,
  *   cache_k / cache_v [B*Hkv][lambda][d] dtype, cache_phik [B*Hkv][lambda][D] f32,
  *   cache_pos [B*Hkv][lambda] int32 (-1 = empty slot),

@@ -422,6 +422,9 @@ class LolaLayer:
         self._check_tensor(parents, (n,), torch.int32, "parents", device=self.buf.device)
         if src.buf.device != self.buf.device:
             raise ValueError(f"src is on {src.buf.device}, expected {self.buf.device}")
+        if torch.cuda.current_device() != self.buf.device.index:
+            with torch.cuda.device(self.buf.device):
+                return self.fork(parents, src, stream)
         _check(lib().lola_state_fork(self.handle, src.handle, c_void_p(parents.data_ptr()), n, _stream(stream)))
         self.B = n
 

@@ -33,7 +33,7 @@ int check_config(const lola_attn_config* c) {
     if (c->d != 64 && c->d != 128) return report(LOLA_ERR_UNSUPPORTED, "d=%d (64 or 128)", c->d);
     if (c->dtype != LOLA_DTYPE_F32 && c->dtype != LOLA_DTYPE_BF16)
         return report(LOLA_ERR_INVALID_ARG, "dtype=%d", c->dtype);
-    if (!(c->scale > 0.f) || !std::isfinite(c->scale))
+    if (!(c->scale > 0.f) || !std::isfinite(c->scale * 1.4426950408889634f))
         return report(LOLA_ERR_INVALID_ARG, "scale=%g must be positive and finite", (double)c->scale);
     const int e = c->dtype == LOLA_DTYPE_BF16 ? 2 : 4;
     const struct { const char* what; long long stride, size; bool zero_ok; } st[] = {

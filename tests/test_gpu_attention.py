@@ -316,6 +316,45 @@ def test_captured_and_replayed_with_other_lengths(T):
                 assert bool(((got.double() - want[0]).abs() <= want[2]).all())
 
 
+def test_captured_with_own_keys_beside_the_shared_ones():
+    """Enough rows that the shared keys' tiles and the own keys run at the same time; two such calls on two
+    streams as well."""
+    B, P, L, Hq, Hkv, d = 40, 900, 130, 16, 2, 64
+    q, k, v = (normal(i, B, n, h, d, dtype=BF16) for i, n, h in ((1, 1, Hq), (2, L, Hkv), (3, L, Hkv)))
+    kp, vp = normal(4, P, Hkv, d, dtype=BF16), normal(5, P, Hkv, d, dtype=BF16)
+    n = torch.full((B,), L, dtype=torch.int32, device="cuda")
+    lola.prefix_attention(q, kp, vp, k, v, own_len=n)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y = lola.prefix_attention(q, kp, vp, k, v, own_len=n)
+    for seed in (7, 8, 9):
+        n.copy_(torch.randint(0, L + 1, (B,), generator=torch.Generator("cuda").manual_seed(seed), device="cuda"))
+        q.copy_(normal(seed, *q.shape, dtype=BF16))
+        g.replay()
+        torch.cuda.synchronize()
+        want = formula(q, kp, vp, k, v, n)
+        assert bool(((y.double() - want[0]).abs() <= want[2]).all())
+    one = lola.prefix_attention(q, kp, vp, k, v, own_len=n)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = [lola.prefix_attention(q, kp, vp, k, v, own_len=n, stream=s) for _ in range(4) for s in streams]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, one) for x in got)
+
+
+def test_own_scratch_too_small_or_misplaced_is_refused():
+    q, k = normal(1, 2, 1, 8, 128, dtype=BF16), normal(2, 2, 5000, 2, 128, dtype=BF16)
+    n = lola.attention_workspace(q, k)
+    assert n > 0
+    ws = torch.empty(n + 256, dtype=torch.uint8, device="cuda")
+    with pytest.raises(lola.LolaError, match="BUF_TOO_SMALL"):
+        lola.cross_attention(q, k, k, workspace=ws[:n - 1])
+    with pytest.raises(lola.LolaError, match="256-byte"):
+        lola.cross_attention(q, k, k, workspace=ws[16:])
+    check(*run_cross(q, k, k, workspace=ws), formula(q, None, None, k, k))
+
+
 def test_refusals():
     q, k = normal(1, 2, 3, 4, 64, dtype=BF16), normal(2, 2, 9, 2, 64, dtype=BF16)
     f = lola.cross_attention
