@@ -127,7 +127,8 @@ size_t plan_attn(AttnArgs& a, int num_sms) {
         if (*chunk == 0) *chunk = unit;
         *parts = n > 0 ? (int)tiles(n, *chunk) : 1;
     };
-    // f32: parts of at least 128 keys, four CTAs per SM (two at a time: ragged lengths even out); bf16 tiles: one per SM, four tiles of 128 keys.
+    // f32: parts of at least 128 keys, four CTAs per SM (two at a time: ragged lengths even out); bf16: one
+    // CTA per SM, parts of at least four tiles of 128 keys.
     auto cut_tiles = [&](long long n0, long long n1, long long r, long long heads, int* parts, int* chunk) {
         long long c;
         if (f32) {

@@ -175,173 +175,173 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
     if (tid == 0 && tmem != 0) *abort_flag = 1;
     // registers: 256 x 208 + 128 x 88 = the 384 x 168 of the launch
     if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (warp == 8) {
-        // ---- K and V tiles: K(j), V(j), K(j + 1), ... into consecutive ring stages ----
-        if (lane == 0) {
-            unsigned n = 0;                       // tiles loaded so far
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (warp == 8) {
+            // ---- K and V tiles: K(j), V(j), K(j + 1), ... into consecutive ring stages ----
+            if (lane == 0) {
+                unsigned n = 0;                       // tiles loaded so far
+                bool ok = true;
+                for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
+                    const TcItem x = tc_item(p, i);
+                    for (int jj = 2 * x.j0; jj < 2 * x.j1 && ok; ++jj, ++n) {
+                        const int s = n % NST, j = jj >> 1;
+                        if (n >= NST) ok = tc_wait(&mbar[Sh::FREE + s], (n / NST - 1) & 1, abort_flag);
+                        if (!ok) break;
+                        const bool sh = j < x.nt0;
+                        const int which = (sh ? 0 : 2) + (jj & 1);
+                        tc_expect(&mbar[Sh::FULL + s], Sh::ST);
+                        tc_tma(ring + s * Sh::ST, &p.map[which], &mbar[Sh::FULL + s], (sh ? j : j - x.nt0) * kTcKeys,
+                               x.g * p.mh[which], x.b * p.mb[which]);
+                    }
+                }
+                if (!ok)                              // given up: the copies in flight still land in this CTA's memory
+                    for (unsigned m = n > NST ? n - NST : 0; m < n; ++m)
+                        (void)umma::mbar_wait(&mbar[Sh::FULL + m % NST], (m / NST) & 1, 1000000000ull);
+            }
+        } else if (warp == 9) {
+            // ---- products ----
+            constexpr uint32_t idS = umma::idesc(umma::kBF16, kTcRows, kTcKeys, false, false);
+            constexpr uint32_t idO = umma::idesc(umma::kBF16, kTcRows, DIM, false, true);
+            const uint64_t dQ = umma::sdesc_sw128(umma::smem_addr(sQ), 16, 1024);
+            const uint64_t dK = umma::sdesc_sw128(umma::smem_addr(ring), 16, 1024);
+            const uint64_t dV = umma::sdesc_sw128(umma::smem_addr(ring), kTcKeys * 128, 1024);
+            // S of row tile T from the key tile in stage ST.  Q and K: a step of 16 dims is 32 bytes inside
+            // a 128-byte half row, the next half 128 rows on.
+            auto scores = [&](auto T, auto ST, bool last) {
+                constexpr int t = decltype(T)::v, st = decltype(ST)::v;
+                if (!tc_elect()) return;
+                constexpr int q0 = t * (Sh::QB / 16), k0 = st * (Sh::ST / 16);
+                // (a loop of few registers: unrolled, its descriptors would all be kept across the loop over the tiles)
+#pragma unroll 1
+                for (int h = 0; h < DIM / 64; ++h)
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks) {
+                        const int step = h * kTcRows * 8 + ks * 2;
+                        umma::mma_bf16(Sh::TS + 128 * t, dQ + (uint64_t)(q0 + step), dK + (uint64_t)(k0 + step), idS, h + ks > 0);
+                    }
+                umma::commit(&mbar[Sh::SFULL + t]);
+                if (last) umma::commit(&mbar[Sh::QFREE + t]);
+            };
+            // O of row tile T (+)= P V, V in stage ST
+            auto values = [&](auto T, auto ST, bool first, bool last) {
+                constexpr int t = decltype(T)::v, st = decltype(ST)::v;
+                if (!tc_elect()) return;
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int k4 = 0; k4 < kTcKeys / 32; ++k4) {
+                        const int ks = h * (kTcKeys / 32) + k4;
+                        umma::mma_f16_ts(Sh::TO + 128 * t, Sh::TS + 128 * t + 8 * ks, dV + (uint64_t)(st * (Sh::ST / 16) + ks * 128),
+                                         idO, ks > 0 || !first);
+                    }
+                if (last) umma::commit(&mbar[Sh::OFULL + t]);
+            };
+            auto release = [&](auto ST) {
+                if (tc_elect()) umma::commit(&mbar[Sh::FREE + decltype(ST)::v]);
+            };
+            auto wait = [&](int i, unsigned parity) { return tc_wait_warp(&mbar[i], parity & 1, abort_flag); };
+            // Key tile number g of this CTA sits in stages 2 (g % 2) and 2 (g % 2) + 1.
+            unsigned g = 0, np[2] = {0, 0}, nq[2] = {0, 0};
+            bool ok = true;
+            // the first scores of an item
+            auto open = [&](auto PAR, int nr, int nt) {
+                constexpr int par = decltype(PAR)::v;
+                ok = wait(Sh::FULL + 2 * par, g >> 1);
+                auto row_tile = [&](auto T) {
+                    constexpr int t = decltype(T)::v;
+                    if (t >= nr || !ok) return;
+                    ok = wait(Sh::QFULL + t, nq[t]++);
+                    if (!ok) return;
+                    umma::fence_after_sync();
+                    scores(TcInt<t>{}, TcInt<2 * par>{}, nt == 1);
+                };
+                row_tile(TcInt<0>{});
+                row_tile(TcInt<1>{});
+                if (ok) release(TcInt<2 * par>{});
+            };
+            // values of tile j (parity PAR) and scores of the next, row tile by row tile
+            auto step = [&](auto PAR, int nr, int nt, int j) {
+                constexpr int par = decltype(PAR)::v;
+                const bool more = j + 1 < nt;
+                ok = wait(Sh::FULL + 2 * par + 1, g >> 1);
+                if (more && ok) ok = wait(Sh::FULL + 2 * (1 - par), (g + 1) >> 1);
+                auto row_tile = [&](auto T) {
+                    constexpr int t = decltype(T)::v;
+                    if (t >= nr || !ok) return;
+                    ok = wait(Sh::PFULL + t, np[t]++);
+                    if (!ok) return;
+                    umma::fence_after_sync();
+                    values(TcInt<t>{}, TcInt<2 * par + 1>{}, j == 0, !more);
+                    if (more) scores(TcInt<t>{}, TcInt<2 * (1 - par)>{}, j + 2 == nt);
+                };
+                row_tile(TcInt<0>{});
+                row_tile(TcInt<1>{});
+                if (!ok) return;
+                release(TcInt<2 * par + 1>{});
+                if (more) release(TcInt<2 * (1 - par)>{});
+            };
+            for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
+                const TcItem x = tc_item(p, i);
+                const int nt = x.j1 - x.j0, nr = x.two ? 2 : 1;
+                if (nt == 0) continue;
+                if (g & 1) open(TcInt<1>{}, nr, nt);
+                else open(TcInt<0>{}, nr, nt);
+                for (int j = 0; j < nt && ok; ++j, ++g) {
+                    if (g & 1) step(TcInt<1>{}, nr, nt, j);
+                    else step(TcInt<0>{}, nr, nt, j);
+                }
+            }
+            if (tc_elect()) umma::commit(&mbar[Sh::DONE]);        // nothing may be in flight when tensor memory is given back
+            if (!umma::mbar_wait(&mbar[Sh::DONE], 0, 4000000000ull)) *abort_flag = 1;
+        } else {
+            // ---- queries: 128-byte swizzled, block kb holds dims 64 kb .. 64 kb + 63 of every row ----
+            constexpr int NC = DIM / 8;
+            unsigned nq[2] = {0, 0};
             bool ok = true;
             for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
                 const TcItem x = tc_item(p, i);
-                for (int jj = 2 * x.j0; jj < 2 * x.j1 && ok; ++jj, ++n) {
-                    const int s = n % NST, j = jj >> 1;
-                    if (n >= NST) ok = tc_wait(&mbar[Sh::FREE + s], (n / NST - 1) & 1, abort_flag);
-                    if (!ok) break;
-                    const bool sh = j < x.nt0;
-                    const int which = (sh ? 0 : 2) + (jj & 1);
-                    tc_expect(&mbar[Sh::FULL + s], Sh::ST);
-                    tc_tma(ring + s * Sh::ST, &p.map[which], &mbar[Sh::FULL + s], (sh ? j : j - x.nt0) * kTcKeys,
-                           x.g * p.mh[which], x.b * p.mb[which]);
-                }
-            }
-            if (!ok)                              // given up: the copies in flight still land in this CTA's memory
-                for (unsigned m = n > NST ? n - NST : 0; m < n; ++m)
-                    (void)umma::mbar_wait(&mbar[Sh::FULL + m % NST], (m / NST) & 1, 1000000000ull);
-        }
-    } else if (warp == 9) {
-        // ---- products ----
-        constexpr uint32_t idS = umma::idesc(umma::kBF16, kTcRows, kTcKeys, false, false);
-        constexpr uint32_t idO = umma::idesc(umma::kBF16, kTcRows, DIM, false, true);
-        const uint64_t dQ = umma::sdesc_sw128(umma::smem_addr(sQ), 16, 1024);
-        const uint64_t dK = umma::sdesc_sw128(umma::smem_addr(ring), 16, 1024);
-        const uint64_t dV = umma::sdesc_sw128(umma::smem_addr(ring), kTcKeys * 128, 1024);
-        // S of row tile T from the key tile in stage ST.  Q and K: a step of 16 dims is 32 bytes inside
-        // a 128-byte half row, the next half 128 rows on.
-        auto scores = [&](auto T, auto ST, bool last) {
-            constexpr int t = decltype(T)::v, st = decltype(ST)::v;
-            if (!tc_elect()) return;
-            constexpr int q0 = t * (Sh::QB / 16), k0 = st * (Sh::ST / 16);
-            // (a loop of few registers: unrolled, its descriptors would all be kept across the loop over the tiles)
-#pragma unroll 1
-            for (int h = 0; h < DIM / 64; ++h)
+                if (i + gridDim.x < p.items) {
+                    // the next item's rows into L2 meanwhile: its copies start when this item's last scores are
+                    // made, and the products wait for them
+                    const TcItem y = tc_item(p, i + gridDim.x);
+                    for (int R = y.r0 + tid - 320; R < min(y.R, y.r0 + 2 * kTcRows); R += 64) {
+                        const bf16* q = (const bf16*)a.q + row_at(a, y.n0, y.g, R).q;
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks) {
-                    const int step = h * kTcRows * 8 + ks * 2;
-                    umma::mma_bf16(Sh::TS + 128 * t, dQ + (uint64_t)(q0 + step), dK + (uint64_t)(k0 + step), idS, h + ks > 0);
-                }
-            umma::commit(&mbar[Sh::SFULL + t]);
-            if (last) umma::commit(&mbar[Sh::QFREE + t]);
-        };
-        // O of row tile T (+)= P V, V in stage ST
-        auto values = [&](auto T, auto ST, bool first, bool last) {
-            constexpr int t = decltype(T)::v, st = decltype(ST)::v;
-            if (!tc_elect()) return;
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int k4 = 0; k4 < kTcKeys / 32; ++k4) {
-                    const int ks = h * (kTcKeys / 32) + k4;
-                    umma::mma_f16_ts(Sh::TO + 128 * t, Sh::TS + 128 * t + 8 * ks, dV + (uint64_t)(st * (Sh::ST / 16) + ks * 128),
-                                     idO, ks > 0 || !first);
-                }
-            if (last) umma::commit(&mbar[Sh::OFULL + t]);
-        };
-        auto release = [&](auto ST) {
-            if (tc_elect()) umma::commit(&mbar[Sh::FREE + decltype(ST)::v]);
-        };
-        auto wait = [&](int i, unsigned parity) { return tc_wait_warp(&mbar[i], parity & 1, abort_flag); };
-        // Key tile number g of this CTA sits in stages 2 (g % 2) and 2 (g % 2) + 1.
-        unsigned g = 0, np[2] = {0, 0}, nq[2] = {0, 0};
-        bool ok = true;
-        // the first scores of an item
-        auto open = [&](auto PAR, int nr, int nt) {
-            constexpr int par = decltype(PAR)::v;
-            ok = wait(Sh::FULL + 2 * par, g >> 1);
-            auto row_tile = [&](auto T) {
-                constexpr int t = decltype(T)::v;
-                if (t >= nr || !ok) return;
-                ok = wait(Sh::QFULL + t, nq[t]++);
-                if (!ok) return;
-                umma::fence_after_sync();
-                scores(TcInt<t>{}, TcInt<2 * par>{}, nt == 1);
-            };
-            row_tile(TcInt<0>{});
-            row_tile(TcInt<1>{});
-            if (ok) release(TcInt<2 * par>{});
-        };
-        // values of tile j (parity PAR) and scores of the next, row tile by row tile
-        auto step = [&](auto PAR, int nr, int nt, int j) {
-            constexpr int par = decltype(PAR)::v;
-            const bool more = j + 1 < nt;
-            ok = wait(Sh::FULL + 2 * par + 1, g >> 1);
-            if (more && ok) ok = wait(Sh::FULL + 2 * (1 - par), (g + 1) >> 1);
-            auto row_tile = [&](auto T) {
-                constexpr int t = decltype(T)::v;
-                if (t >= nr || !ok) return;
-                ok = wait(Sh::PFULL + t, np[t]++);
-                if (!ok) return;
-                umma::fence_after_sync();
-                values(TcInt<t>{}, TcInt<2 * par + 1>{}, j == 0, !more);
-                if (more) scores(TcInt<t>{}, TcInt<2 * (1 - par)>{}, j + 2 == nt);
-            };
-            row_tile(TcInt<0>{});
-            row_tile(TcInt<1>{});
-            if (!ok) return;
-            release(TcInt<2 * par + 1>{});
-            if (more) release(TcInt<2 * (1 - par)>{});
-        };
-        for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
-            const TcItem x = tc_item(p, i);
-            const int nt = x.j1 - x.j0, nr = x.two ? 2 : 1;
-            if (nt == 0) continue;
-            if (g & 1) open(TcInt<1>{}, nr, nt);
-            else open(TcInt<0>{}, nr, nt);
-            for (int j = 0; j < nt && ok; ++j, ++g) {
-                if (g & 1) step(TcInt<1>{}, nr, nt, j);
-                else step(TcInt<0>{}, nr, nt, j);
-            }
-        }
-        if (tc_elect()) umma::commit(&mbar[Sh::DONE]);        // nothing may be in flight when tensor memory is given back
-        if (!umma::mbar_wait(&mbar[Sh::DONE], 0, 4000000000ull)) *abort_flag = 1;
-    } else {
-        // ---- queries: 128-byte swizzled, block kb holds dims 64 kb .. 64 kb + 63 of every row ----
-        constexpr int NC = DIM / 8;
-        unsigned nq[2] = {0, 0};
-        bool ok = true;
-        for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
-            const TcItem x = tc_item(p, i);
-            if (i + gridDim.x < p.items) {
-                // the next item's rows into L2 meanwhile: its copies start when this item's last scores are
-                // made, and the products wait for them
-                const TcItem y = tc_item(p, i + gridDim.x);
-                for (int R = y.r0 + tid - 320; R < min(y.R, y.r0 + 2 * kTcRows); R += 64) {
-                    const bf16* q = (const bf16*)a.q + row_at(a, y.n0, y.g, R).q;
-#pragma unroll
-                    for (int c = 0; c < DIM; c += 64) asm volatile("prefetch.global.L2 [%0];" :: "l"(q + c));
-                }
-            }
-            if (x.j0 == x.j1) continue;
-            for (int t = 0; t < (x.two ? 2 : 1) && ok; ++t) {
-                if (nq[t]) ok = tc_wait(&mbar[Sh::QFREE + t], (nq[t] - 1) & 1, abort_flag);
-                ++nq[t];
-                if (!ok) break;
-                // each lane finds one row, then 32 / NC rows at a time are copied in 16-byte chunks
-#pragma unroll 1
-                for (int r32 = 32 * (warp - 10); r32 < kTcRows; r32 += 64) {
-                    const int R = x.r0 + t * kTcRows + r32 + lane;
-                    const long long at = R < x.R ? row_at(a, x.n0, x.g, R).q : -1;
-#pragma unroll
-                    for (int k = 0; k < NC; ++k) {
-                        const int rr = k * (32 / NC) + lane / NC, c = lane % NC, r = r32 + rr;
-                        const long long from = __shfl_sync(0xffffffffu, at, rr);
-                        umma::cp_async16_zfill(sQ + t * Sh::QB + (c >> 3) * (kTcRows * 128) + umma::sw128_off(r, c & 7),
-                                               (const bf16*)a.q + (from < 0 ? 0 : from) + 8 * c, from >= 0);
+                        for (int c = 0; c < DIM; c += 64) asm volatile("prefetch.global.L2 [%0];" :: "l"(q + c));
                     }
                 }
-                umma::cp_async_commit();
-            }
-            if (!ok) break;
-            if (x.two) {
-                umma::cp_async_wait<1>();
+                if (x.j0 == x.j1) continue;
+                for (int t = 0; t < (x.two ? 2 : 1) && ok; ++t) {
+                    if (nq[t]) ok = tc_wait(&mbar[Sh::QFREE + t], (nq[t] - 1) & 1, abort_flag);
+                    ++nq[t];
+                    if (!ok) break;
+                    // each lane finds one row, then 32 / NC rows at a time are copied in 16-byte chunks
+#pragma unroll 1
+                    for (int r32 = 32 * (warp - 10); r32 < kTcRows; r32 += 64) {
+                        const int R = x.r0 + t * kTcRows + r32 + lane;
+                        const long long at = R < x.R ? row_at(a, x.n0, x.g, R).q : -1;
+#pragma unroll
+                        for (int k = 0; k < NC; ++k) {
+                            const int rr = k * (32 / NC) + lane / NC, c = lane % NC, r = r32 + rr;
+                            const long long from = __shfl_sync(0xffffffffu, at, rr);
+                            umma::cp_async16_zfill(sQ + t * Sh::QB + (c >> 3) * (kTcRows * 128) + umma::sw128_off(r, c & 7),
+                                                   (const bf16*)a.q + (from < 0 ? 0 : from) + 8 * c, from >= 0);
+                        }
+                    }
+                    umma::cp_async_commit();
+                }
+                if (!ok) break;
+                if (x.two) {
+                    umma::cp_async_wait<1>();
+                    umma::fence_async_smem();
+                    umma::mbar_arrive(&mbar[Sh::QFULL]);
+                }
+                umma::cp_async_wait<0>();
                 umma::fence_async_smem();
-                umma::mbar_arrive(&mbar[Sh::QFULL]);
+                umma::mbar_arrive(&mbar[Sh::QFULL + (x.two ? 1 : 0)]);
             }
             umma::cp_async_wait<0>();
-            umma::fence_async_smem();
-            umma::mbar_arrive(&mbar[Sh::QFULL + (x.two ? 1 : 0)]);
         }
-        umma::cp_async_wait<0>();
-    }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         // ---- softmax and output of row tile t ----
