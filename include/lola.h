@@ -235,8 +235,9 @@ int lola_sre_map(lola_state* st, const void* k, const void* v, int T, float* sre
  * wall time) that gives up sets the word, finishes without that result and
  * returns.  Returns LOLA_ERR_TIMEOUT if any kernel of this state has set it
  * since the last init or reset (the outputs of those calls are not valid;
- * lola_state_reset clears the word), LOLA_ERR_CUDA if the stream reports an
- * error, LOLA_OK otherwise. */
+ * lola_state_reset clears the word), LOLA_ERR_INVALID_ARG if a fork into this
+ * state had a parent outside its source (see lola_state_fork), LOLA_ERR_CUDA if
+ * the stream reports an error, LOLA_OK otherwise. */
 int lola_state_check(lola_state* st, void* stream);
 
 /* Number of sequences that later calls process: the first n of the config's B

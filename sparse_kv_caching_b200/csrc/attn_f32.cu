@@ -81,6 +81,7 @@ __global__ void __launch_bounds__(kFrThreads) attn_f32_rows_kernel(const __grid_
     __shared__ float so[kFrThreads / 32][kFrRows][DIM];
     __shared__ float2 sml[kFrThreads / 32][kFrRows];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c8 = lane & 7, grp = lane >> 3;
+    attn_let_next_begin();
     const F32Work w = f32_work(a, blockIdx.x, 0);
     const int r0 = blockIdx.y * kFrRows;
     float4 q[kFrRows][NF], o[kFrRows][NF];
@@ -202,6 +203,7 @@ __global__ void __launch_bounds__(kFtThreads, 2) attn_f32_tile_kernel(const __gr
     float *sq = fs + Sh::Q, *sp = fs + Sh::PP;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int row_tiles = ((packed ? a.B : 1) * a.T * a.Gq + kFtRows - 1) / kFtRows;
+    attn_let_next_begin();
     const F32Work w = f32_work(a, blockIdx.x / row_tiles, packed);     // neighbours read the same keys
     const int r0 = (blockIdx.x % row_tiles) * kFtRows;
     for (int i = tid; i < kFtRows * DIM / 4; i += kFtThreads) {
