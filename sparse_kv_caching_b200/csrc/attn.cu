@@ -48,8 +48,8 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
             if (c0[1] == c1[1]) c1[1] = -1;
             else p1 = a.parts_shared;
         }
-        if (!a.part_o) {
-            if (c1[1] < 0) return;             // written whole
+        if (!a.part_o) {                       // one group a row, shared or own
+            if (c1[0] < 0 && c1[1] < 0) return;        // written whole
             p1 = p0;
         }
     }
