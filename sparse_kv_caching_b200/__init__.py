@@ -217,6 +217,8 @@ def _attn_plan(q, k, v, kp, vp, lens, lens_name, y, lse, scale):
 
 
 def _attention(q, kp, vp, k, v, lens, lens_name, scale, y, lse, workspace, stream):
+    if scale is not None:
+        scale = c_float(scale).value    # the plan is looked up by this value (a tensor would be by its identity)
     try:
         cfg, need = _attn_plan(_what(q), _what(k), _what(v), None if kp is None else _what(kp),
                                None if vp is None else _what(vp), None if lens is None else _what(lens), lens_name,
