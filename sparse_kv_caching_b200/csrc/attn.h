@@ -9,8 +9,6 @@
 // one softmax: they are either walked one after the other by the same CTA, or
 // reduced apart and joined by their log-sum-exp.
 #pragma once
-#include <atomic>
-
 #include "lola_internal.h"
 
 namespace lola {
@@ -76,18 +74,6 @@ cudaError_t attn_error_word(int* word, cudaStream_t s);
 // begins before earlier work on the stream has ended.  attn_let_next_begin: the next kernel may be scheduled.
 __device__ __forceinline__ void attn_wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void attn_let_next_begin() { asm volatile("griddepcontrol.launch_dependents;"); }
-// Lets a kernel use `bytes` of dynamic shared memory, asked of the driver once on each device (bit i of *done).
-template <typename Kernel>
-cudaError_t attn_allow_smem(Kernel kernel, int bytes, std::atomic<unsigned long long>* done) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
-    if (done->load(std::memory_order_relaxed) & bit) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_relaxed);
-    return e;
-}
 template <typename Args>
 cudaError_t attn_launch(void (*kernel)(const Args), unsigned grid, unsigned threads, size_t smem, bool behind, cudaStream_t s,
                         const Args& args) {

@@ -349,7 +349,7 @@ template <int DIM>
 static cudaError_t launch_tile_t(const AttnArgs& a, int packed, cudaStream_t s) {
     constexpr int bytes = F32Tile<DIM>::WORDS * 4;
     static std::atomic<unsigned long long> done{0};
-    cudaError_t e = attn_allow_smem(attn_f32_tile_kernel<DIM>, bytes, &done);
+    cudaError_t e = allow_smem(attn_f32_tile_kernel<DIM>, bytes, &done);
     if (e != cudaSuccess) return e;
     const int rows = (packed ? a.B : 1) * a.T * a.Gq;
     const unsigned grid = (rows + kFtRows - 1) / kFtRows * (packed ? a.parts_shared * a.Hkv : a.parts_own * a.Hkv * a.B);

@@ -416,7 +416,7 @@ template <int DIM>
 static cudaError_t launch_rows_t(const AttnArgs& a, cudaStream_t s) {
     using Sh = RowsShape<DIM>;
     static std::atomic<unsigned long long> done{0};
-    cudaError_t e = attn_allow_smem(attn_rows_kernel<DIM>, Sh::BYTES, &done);
+    cudaError_t e = allow_smem(attn_rows_kernel<DIM>, Sh::BYTES, &done);
     if (e != cudaSuccess) return e;
     const int per_head = a.even ? a.even : (a.by_shared == AttnBy::rows) + (a.by_own == AttnBy::rows ? a.B : 0);
     return attn_launch(attn_rows_kernel<DIM>, (unsigned)per_head * a.Hkv, kRwWarps * 32, Sh::BYTES, a.beside != 0, s, a);

@@ -547,7 +547,7 @@ template <int DIM>
 cudaError_t launch_tc_t(const TcArgs& p, int num_sms, cudaStream_t s) {
     using Sh = TcShape<DIM>;
     static std::atomic<unsigned long long> done{0};
-    cudaError_t e = attn_allow_smem(attn_tc_kernel<DIM>, Sh::BYTES, &done);
+    cudaError_t e = allow_smem(attn_tc_kernel<DIM>, Sh::BYTES, &done);
     if (e != cudaSuccess) return e;
     attn_tc_kernel<DIM><<<p.items < num_sms ? p.items : num_sms, kTcThreads, Sh::BYTES, s>>>(p);
     return cudaGetLastError();

@@ -184,14 +184,26 @@ __global__ void __launch_bounds__(kForkThreads, 2) fork_in_place_kernel(const __
     }
 }
 
+// Shared memory of an in-place fork of n sequences.  Every sequence may be a hazard: 32 threads' slots have
+// to fit, 16 bytes wide up to 200 KB, else 4.  Up to 128 sequences that is the 64 KB with which three CTAs
+// share an SM.
+constexpr bool fork_wide(int n) { return n * 32 * 16 <= 200 * 1024; }
+constexpr int fork_slot_bytes(int n) {
+    const int b = n * 32 * (fork_wide(n) ? 16 : 4);
+    return b > 64 * 1024 ? b : 64 * 1024;
+}
+constexpr int fork_smem_bytes(int n) { return 4 * ((n + 3) & ~3) * (int)sizeof(int) + fork_slot_bytes(n); }
+constexpr int fork_smem_most() {
+    int most = 0;
+    for (int n = 1; n <= kForkInPlaceMax; ++n)
+        if (fork_smem_bytes(n) > most) most = fork_smem_bytes(n);
+    return most;
+}
+static_assert(fork_smem_most() + 64 <= 227 * 1024, "shared memory");
+
 cudaError_t launch_fork(ForkArgs a, int num_sms, cudaStream_t s) {
     const bool in_place = a.seg[0].src == a.seg[0].dst;
-    // In place every sequence may be a hazard: 32 threads' slots have to fit, 16 bytes wide up to
-    // 200 KB, else 4.  Up to 128 sequences that is the 64 KB with which three CTAs share an SM.
-    size_t slot_bytes = 64 * 1024;
-    a.wide = 1;
-    if ((size_t)a.n * 32 * 16 > 200 * 1024) a.wide = 0;
-    if ((size_t)a.n * 32 * (a.wide ? 16 : 4) > slot_bytes) slot_bytes = (size_t)a.n * 32 * (a.wide ? 16 : 4);
+    a.wide = fork_wide(a.n);
     a.tiles = 0;
     for (int i = 0; i < a.nseg; ++i) {
         ForkSeg& sg = a.seg[i];
@@ -206,10 +218,10 @@ cudaError_t launch_fork(ForkArgs a, int num_sms, cudaStream_t s) {
         fork_kernel<<<dim3(grid((3LL * num_sms + groups - 1) / groups), groups), kForkThreads, 0, s>>>(a);
         return cudaGetLastError();
     }
-    const size_t smem = 4 * (size_t)((a.n + 3) & ~3) * sizeof(int) + slot_bytes;
-    cudaError_t e = cudaFuncSetAttribute(fork_in_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<unsigned long long> done{0};
+    cudaError_t e = allow_smem(fork_in_place_kernel, fork_smem_most(), &done);
     if (e != cudaSuccess) return e;
-    fork_in_place_kernel<<<grid(3LL * num_sms), kForkThreads, smem, s>>>(a, (int)slot_bytes);
+    fork_in_place_kernel<<<grid(3LL * num_sms), kForkThreads, fork_smem_bytes(a.n), s>>>(a, fork_slot_bytes(a.n));
     return cudaGetLastError();
 }
 

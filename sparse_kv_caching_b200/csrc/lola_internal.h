@@ -20,6 +20,8 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace lola {
 
 constexpr int kThreads = 512;
@@ -132,6 +134,21 @@ struct ForkArgs {
 // Sets the text of lola_last_error_string and returns code; adds to lola_launch_count.
 int report(int code, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
 void count_launches(int kernels);
+
+// Lets a kernel use `bytes` of dynamic shared memory, asked of the driver once on each device (bit i of
+// *done).  `bytes` is the most that any launch of the kernel takes: the limit is the device's, so a smaller one
+// asked for by another thread's launch would make a larger launch fail.
+template <typename Kernel>
+cudaError_t allow_smem(Kernel kernel, int bytes, std::atomic<unsigned long long>* done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+    if (done->load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 // Launchers (each returns cudaGetLastError() of its launch).
 cudaError_t launch_fork(ForkArgs a, int num_sms, cudaStream_t s);
