@@ -3,10 +3,10 @@
 //
 // Mathematics: one pass over tiles of 128 keys with a running reference r of the
 // softmax exponents.  S = Q K^T (tensor cores, f32); P = 2^(c S - r), c =
-// scale log2(e); l += row sums of P in f32; O += P V with P rounded to bf16 (its
+// scale log2(e), r = c m; l += row sums of P in f32; O += P V with P rounded to bf16 (its
 // product's type; half a step, 2^-8 of each weight, averages out over the keys,
-// while f16 weights would need V converted).  r is raised only when a row's
-// maximum passes r + 8, which keeps P below 2^8 and makes rescaling O rare.
+// while f16 weights would need V converted).  m is raised only when a row's
+// maximum passes m + 8 / c, which keeps P below 2^8 and makes rescaling O rare.
 //
 // Bound: the tensor cores (4 d operations per row and key) and, as hard, the
 // exponentials: a 128 x 128 tile costs 1056 cycles of products and 1024 of the
@@ -377,12 +377,25 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                 for (int u = 4; u < kTcKeys; u += 8)
 #pragma unroll
                     for (int v = 0; v < 4; ++v) m4[v] = fmaxf(m4[v], u + 4 < kTcKeys ? fmaxf(s[u + v], s[u + v + 4]) : s[u + v]);
-                float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c2;
+                const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                 float f = 1.f;
                 bool raise = false;
                 if (m == -INFINITY) m = mx;       // nothing read yet
-                else if (mx > m + 8.f) { f = tc_ex2(m - mx); m = mx; raise = true; }
-                const float ref = m == -INFINITY ? 0.f : m;
+                else if ((mx - m) * c2 > 8.f) {
+                    f = tc_ex2((m - mx) * c2);
+                    m = mx;
+                    raise = true;
+                }
+                // c s - r in one rounding leaves c m - r, r's own rounding: far below 1 for the scores of a
+                // model, but the exponent of a huge one could overflow.  Those rows subtract first.
+                float from = m == -INFINITY ? 0.f : m, ref = from * c2;
+                const bool huge = !(fabsf(ref) < 1048576.f);
+                if (huge) ref = 0.f;
+                else from = 0.f;
+                if (__any_sync(0xffffffffu, huge)) {
+#pragma unroll
+                    for (int u = 0; u < kTcKeys; ++u) s[u] -= from;
+                }
                 if (__any_sync(0xffffffffu, raise)) {
                     // every product before S(j) is complete: O is free
                     l *= f;
@@ -445,7 +458,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                 umma::fence_after_sync();
             }
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            const float l2 = l == 0.f ? -INFINITY : m + log2f(l);
+            const float l2 = l == 0.f ? -INFINITY : fmaf(m, c2, log2f(l));
             // The row's place is found again: kept across the loop it would cost registers there.
             int Ro = row_ok ? R : 0;
             asm volatile("" : "+r"(Ro));
