@@ -718,7 +718,7 @@ int lola_state_check(lola_state* st, void* stream) {
     if (e != cudaSuccess) return cuda_fail(e, "reading the device error word");
     if (word == 2)
         return fail(LOLA_ERR_INVALID_ARG, "a fork's parent was outside the source's sequences; the sequences it "
-                    "should have filled are not valid: fork them again from a valid state, or reset");
+                    "should have filled are not valid: reset the state, then fork again");
     if (word != 0)
         return fail(LOLA_ERR_TIMEOUT, "a bounded device-side wait gave up (error word 0x%x); the results of "
                     "the calls since the last reset are not valid: reset the state", (unsigned)word);
