@@ -718,8 +718,8 @@ __global__ void __launch_bounds__(256) residual_init_kernel(const __grid_constan
 template <int DIM, int DH, int GQM, typename TIn>
 static cudaError_t launch_dec_g(const DecodeArgs& a, cudaStream_t s) {
     const size_t bytes = (size_t)dec_offsets(DIM, DH, a.dm.Gq, a.dm.lam, a.dm.eta, (int)sizeof(TIn)).total * 4;
-    cudaError_t e = cudaFuncSetAttribute(decode_kernel<DIM, DH, GQM, TIn>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    static std::atomic<unsigned long long> done{0};
+    cudaError_t e = allow_smem(decode_kernel<DIM, DH, GQM, TIn>, 0, &done);
     if (e != cudaSuccess) return e;
     decode_kernel<DIM, DH, GQM, TIn><<<a.dm.S, kDecThreads, bytes, s>>>(a);
     return cudaGetLastError();

@@ -1029,8 +1029,8 @@ size_t scan_smem_bytes(const Dims& dm) {
 template <int D, int DV, typename TIn>
 static cudaError_t launch_scan_t(const PrefillArgs& a, cudaStream_t s) {
     const size_t bytes = scan_smem_bytes(a.dm);
-    cudaError_t e = cudaFuncSetAttribute(scan_kernel<D, DV, TIn>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    static std::atomic<unsigned long long> done{0};
+    cudaError_t e = allow_smem(scan_kernel<D, DV, TIn>, 0, &done);
     if (e != cudaSuccess) return e;
     scan_kernel<D, DV, TIn><<<a.dm.S, kThreads, bytes, s>>>(a);
     return cudaGetLastError();
@@ -1050,7 +1050,8 @@ template <int D, int DV, int NCL, typename TIn>
 static cudaError_t launch_scan_cl_t(const PrefillArgs& a, cudaStream_t s) {
     const size_t bytes = scan_cl_smem_bytes(a.dm, DV / NCL);
     auto kern = scan_cl_kernel<D, DV, NCL, TIn>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    static std::atomic<unsigned long long> done{0};
+    cudaError_t e = allow_smem(kern, 0, &done);
     if (e == cudaSuccess && NCL > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -1111,7 +1112,8 @@ template <int D, int DV, int NCL, typename TIn>
 static cudaError_t launch_scan_cg_t(const PrefillArgs& a, cudaStream_t s) {
     const size_t bytes = scan_cg_smem_bytes(a.dm, DV / NCL);
     auto kern = scan_cg_kernel<D, DV, NCL, TIn>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    static std::atomic<unsigned long long> done{0};
+    cudaError_t e = allow_smem(kern, 0, &done);
     if (e == cudaSuccess && NCL > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};

@@ -826,7 +826,8 @@ template <int D, int DV, int NCL, typename TIn>
 static cudaError_t launch_tc_chain_t(const PrefillArgs& a, cudaStream_t s) {
     const size_t bytes = scan_tc_smem_bytes(a.dm, NCL);
     auto kern = scan_tc_kernel<D, DV, NCL, TIn>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    static std::atomic<unsigned long long> done{0};
+    cudaError_t e = allow_smem(kern, 0, &done);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.dm.S * NCL);

@@ -251,8 +251,8 @@ int selftest_tmem_cols(int mode, int N, int K) {
 cudaError_t launch_selftest(int mode, const void* A, const void* B, float* C, int M, int N, int K, int* err,
                             cudaStream_t s) {
     const size_t bytes = selftest_smem(mode, M, N, K);
-    cudaError_t e = cudaFuncSetAttribute(umma_selftest_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)bytes);
+    static std::atomic<unsigned long long> done{0};
+    cudaError_t e = allow_smem(umma_selftest_kernel, 0, &done);
     if (e != cudaSuccess) return e;
     SelftestArgs a{mode, M, N, K, A, B, C, err};
     umma_selftest_kernel<<<1, 128, bytes, s>>>(a);
