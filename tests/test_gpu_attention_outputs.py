@@ -93,3 +93,19 @@ def test_shared_keys_alone_captured_and_replayed(B, T, N, Hq, Hkv):
         g.replay()
         torch.cuda.synchronize()
         check(y, lse, formula(q, None, None, kb, vb))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,G", [(2, 4), (6, 3), (200, 2)])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_keys_behind_the_own_position_do_not_matter(dtype, T, G, bad):
+    """NaN and infinities in the key of each sequence's last token: every query but the last is as without."""
+    B, L, Hkv, d = 3, 333, 2, 128
+    q, k, v = normal(1, B, T, G * Hkv, d, dtype=dtype), normal(2, B, L, Hkv, d, dtype=dtype), normal(3, B, L, Hkv, d, dtype=dtype)
+    kp, vp = normal(4, 600, Hkv, d, dtype=dtype), normal(5, 600, Hkv, d, dtype=dtype)
+    n = ints(333, 230, 205)
+    want = formula(q, kp, vp, k, v, n)
+    for b in range(B):
+        k[b, int(n[b]) - 1] = bad
+    y, lse = prefix(q, kp, vp, k, v, n)
+    check(y[:, :-1], lse[:, :-1], tuple(x[:, :-1] for x in want))
