@@ -10,6 +10,8 @@
 #include <string>
 #include <vector>
 
+#include "fork.h"
+#include "host.h"
 #include "lola.h"
 #include "lola_internal.h"
 

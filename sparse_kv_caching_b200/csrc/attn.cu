@@ -10,6 +10,9 @@
 
 namespace lola {
 
+__device__ __forceinline__ void store_as(float* p, float x) { *p = x; }
+__device__ __forceinline__ void store_as(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
 // The parts of a row put together: with L_p the log2-sum-exp of part p and O_p its
 // normalised sum, L = log2 sum 2^L_p and y = sum 2^(L_p - L) O_p.  One warp per row;
 // the parts were just written and come from L2.
@@ -183,8 +186,8 @@ size_t plan_attn(AttnArgs& a, int num_sms) {
     if (!f32 && (a.by_own == AttnBy::rows || a.by_shared == AttnBy::rows)) {
         // The shared keys' tiles are bound by the tensor cores and by their own begin and end, the own keys
         // by HBM, or by how fast an SM turns them over: they run at the same time on SMs of their own, in
-        // the shares that end together.  Measured, in us: 1.75 for each pair of row tiles and key tile and 20
-        // for the rest; 0.04 MB per us and SM, 5.2 in all, and 5 for the rest.
+        // the shares that end together.  Measured (32 / 8 heads, d 128), in us: 1.75 for each pair of row
+        // tiles and key tile and 20 for the rest; 0.04 MB per us and SM, 5.2 in all, and 5 for the rest.
         long long slots = 2LL * num_sms;
         const long long base = tiles(all_rows, 256) * a.Hkv;
         if (a.by_shared == AttnBy::tiles && a.by_own == AttnBy::rows && base + a.Hkv / 2 < num_sms) {

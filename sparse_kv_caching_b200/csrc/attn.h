@@ -9,6 +9,7 @@
 // one softmax: they are either walked one after the other by the same CTA, or
 // reduced apart and joined by their log-sum-exp.
 #pragma once
+#include "host.h"
 #include "lola_internal.h"
 
 namespace lola {

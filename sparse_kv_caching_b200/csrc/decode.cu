@@ -30,6 +30,7 @@
 // read, the residual update right after P V (the members' value rows still in
 // L2), and last the writes of l's slot and of the ring slot.
 #include "device_common.cuh"
+#include "host.h"
 #include "umma.cuh"
 
 namespace lola {

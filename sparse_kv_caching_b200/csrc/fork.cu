@@ -28,7 +28,8 @@
 //   many hazards a CTA's first threads share all of its slots.
 #include <limits.h>
 
-#include "lola_internal.h"
+#include "fork.h"
+#include "host.h"
 
 namespace lola {
 

@@ -20,8 +20,6 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
-#include <atomic>
-
 namespace lola {
 
 constexpr int kThreads = 512;
@@ -108,55 +106,7 @@ struct SreMapArgs {
     int nc;                // its chunks
 };
 
-// One memory of a fork: rows of seq_bytes, one per sequence, gathered by the parents.
-struct ForkSeg {
-    const char* src;
-    char* dst;
-    long long seq_bytes;
-    long long cols, tile0; // columns per sequence and the memory's first tile (set by the launcher)
-    int wide;              // columns of 16 bytes (else 4)
-};
-constexpr int kForkSegs = 13;          // memories a fork may copy
-constexpr int kForkGroup = 64;         // destination sequences per CTA (between two states)
-constexpr int kForkInPlaceMax = 1500;  // sequences of an in-place fork (shared-memory slots, 32 threads x 4 bytes)
-
-struct ForkArgs {
-    ForkSeg seg[kForkSegs];
-    int nseg;
-    const int* parents;    // [n] device
-    int n, src_B;
-    int* src_err;
-    int* dst_err;          // bit 1: a parent outside [0, src_B)
-    long long tiles;       // set by the launcher, as
-    int wide;              // in place: 16-byte slots (else 4)
-};
-
-// Sets the text of lola_last_error_string and returns code; adds to lola_launch_count.
-int report(int code, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
-void count_launches(int kernels);
-
-// Lets a kernel use up to `bytes` of dynamic shared memory (0: all that a block may have, 227 KB), asked of the
-// driver once on each device (bit i of *done).  The limit belongs to the device: a launch that asked for its own
-// size could lower it under a larger launch of another thread, so `bytes` is the most that any launch takes.
-template <typename Kernel>
-cudaError_t allow_smem(Kernel kernel, int bytes, std::atomic<unsigned long long>* done) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
-    if (done->load(std::memory_order_relaxed) & bit) return cudaSuccess;
-    if (bytes == 0) {
-        cudaFuncAttributes at;
-        if ((e = cudaFuncGetAttributes(&at, kernel)) != cudaSuccess) return e;
-        bytes = 227 * 1024 - (int)at.sharedSizeBytes;
-    }
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_relaxed);
-    return e;
-}
-
 // Launchers (each returns cudaGetLastError() of its launch).
-cudaError_t launch_fork(ForkArgs a, int num_sms, cudaStream_t s);
 cudaError_t launch_phi_keys(const PrefillArgs& a, cudaStream_t s);
 cudaError_t launch_scan(const PrefillArgs& a, cudaStream_t s);
 // The chain on the tensor cores (scan_tc.cu); cudaErrorNotSupported outside its shapes.

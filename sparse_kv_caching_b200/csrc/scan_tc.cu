@@ -44,6 +44,7 @@
 
 #include "chain_common.cuh"
 #include "device_common.cuh"
+#include "host.h"
 #include "umma.cuh"
 
 namespace lola {

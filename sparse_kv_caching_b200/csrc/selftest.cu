@@ -15,6 +15,7 @@
 // the raw f32 values (not rounded down to tf32 first), to check that kind::tf32
 // reads only their top 19 bits.
 #include "device_common.cuh"
+#include "host.h"
 #include "umma.cuh"
 
 namespace lola {
