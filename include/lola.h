@@ -27,6 +27,8 @@
  *   - Return value 0 = LOLA_OK; a negative value is one of the LOLA_ERR_*
  *     codes below and lola_last_error_string() describes it (thread-local).
  *     No entry point aborts the process or traps on the device.
+ *   - Several host threads may call at the same time, each on states, buffers
+ *     and streams of its own (lola_prefill_once_noalloc: see there).
  *   - Feature map phi(x) = [softmax(x W_g), softmax(-x W_g)] (Hedgehog form,
  *     fixed by this library; the pages leave phi as "learned"), D = 2 Dh.
  *   - Sequences of a batch advance in lock step: every call processes the
@@ -273,11 +275,16 @@ int lola_state_fork(lola_state* dst, const lola_state* src, const int* parents, 
  *   lse[b][t][h] = log sum_i exp(scale q . k_i)   (natural log).
  * A row that reads no key gets y = 0 and lse = -infinity.  Keys and values behind
  * a sequence's length never reach a result, whatever they hold (NaN and
- * infinities too).  Values of its later tokens must be finite: a query that
- * does not read them multiplies them by 0.
+ * infinities too), nor do keys of tokens behind a query's own.  Values of those
+ * tokens must be finite: a query that does not read them multiplies them by 0.
  * y is in dtype (its next use is a projection in that type), lse float32.
+ * Forward only: no gradient is computed, nor anything kept for one.
  * Precision: bf16 inputs multiply on the tensor cores with f32 accumulation;
- * f32 inputs, the softmax statistics and the sums are f32.
+ * f32 inputs, the softmax statistics and the sums are f32.  For its product with
+ * v a weight p_i of bf16 inputs is rounded to bf16 (2^-8 of it) where more than 16
+ * query rows of a kv head are taken together, and kept to 2^-16 where fewer are.
+ * scale q.k log2(e) and the sums of v with weights of up to 2^8 (they are normalised
+ * at the end) must stay inside f32's range.
  *
  * Sizes: B, T >= 1; P, L >= 0; Hq % Hkv == 0; d in {64, 128}; scale > 0 and
  * finite; B, Hkv <= 65535; B * T * Hq < 2^31.  Strides are in elements (batch, token, head;
@@ -307,12 +314,15 @@ int lola_attn_workspace(const lola_attn_config* cfg, size_t* bytes);
 /* Attention to an encoder's states of another length: q [B][T][Hq][d], k and v
  * [B][L][Hkv][d]; every query of sequence b reads keys s < kv_len[b] (device
  * int32 [B]; values are clamped to 0..L; NULL: L for every sequence).  P must be
- * 0.  y [B][T][Hq][d] contiguous; lse [B][T][Hq] or NULL. */
+ * 0.  One encoder output for all sequences (batch strides of 0) is read as a
+ * shared prefix is if kv_len is NULL, else by each sequence.
+ * y [B][T][Hq][d] contiguous; lse [B][T][Hq] or NULL. */
 int lola_cross_attention(const lola_attn_config* cfg, const void* q, const void* k, const void* v,
                          const int* kv_len, void* y, float* lse, void* workspace, size_t bytes, void* stream);
 
 /* Attention of sequences that share a prefix of P keys (k_prefix, v_prefix
- * [P][Hkv][d]; read once for the whole batch), each followed by keys of its own
+ * [P][Hkv][d]; read by all their rows as one group, or by each sequence again,
+ * from L2 as a rule, where that is no slower), each followed by keys of its own
  * (k, v [B][L][Hkv][d], of which sequence b has own_len[b]; device int32 [B],
  * clamped to 0..L; NULL: L).  The T queries are the last T tokens of their
  * sequence and causal in it: query t reads the prefix and its own keys

@@ -278,16 +278,18 @@ def cross_attention(q, k, v, kv_len=None, scale=None, y=None, lse=None, workspac
     """Attention to an encoder's states: q [B,T,Hq,d], k/v [B,S,Hkv,d] -> y [B,T,Hq,d] in q's dtype.
 
     Every query of sequence b reads the keys s < kv_len[b] (int32 [B] on the device; all S if
-    None).  scale is 1/sqrt(d) if None.  Any strides with contiguous heads, a batch stride of 0
-    (one encoder output for all sequences, read once) among them.  lse (float32 [B,T,Hq]), if
-    given, receives each row's log-sum-exp.  workspace: scratch to use instead of an allocation
-    (attention_workspace bytes); calls that may overlap need one each."""
+    None).  scale is 1/sqrt(d) if None; a number or a 0-d tensor, read when the call is made.  Any
+    strides with contiguous heads, a batch stride of 0 among them (one encoder output for all
+    sequences, read once for the batch if kv_len is None).  lse (float32 [B,T,Hq]), if given,
+    receives each row's log-sum-exp.  workspace: scratch to use instead of an allocation
+    (attention_workspace bytes); calls that may overlap need one each.  Forward only: y carries no
+    gradient, whatever the inputs require."""
     return _attention(q, None, None, k, v, kv_len, "kv_len", scale, y, lse, workspace, stream)
 
 
 def prefix_attention(q, k_prefix, v_prefix, k, v, own_len=None, scale=None, y=None, lse=None, workspace=None,
                      stream=None):
-    """Attention of a batch that shares a prefix, which is read once for all its sequences.
+    """Attention of a batch that shares a prefix, whose keys all its sequences read together.
 
     q [B,T,Hq,d]: the last T tokens of each sequence; k_prefix/v_prefix [P,Hkv,d]; k/v
     [B,L,Hkv,d]: each sequence's own keys, own_len[b] of them (int32 [B]; all L if None).  Query
@@ -469,8 +471,9 @@ class LolaLayer:
         return {k: (float(ms[i]), int(cnt[i])) for i, k in enumerate(KERNEL_CLASSES)}
 
     def check(self, stream=None) -> None:
-        """Sync point: wait for the stream and raise LolaError (LOLA_ERR_TIMEOUT) if a bounded
-        device-side wait of this state gave up since the last reset."""
+        """Sync point: wait for the stream and raise LolaError if a bounded device-side wait of this
+        state gave up (LOLA_ERR_TIMEOUT) or a fork into it had a parent outside its source
+        (LOLA_ERR_INVALID_ARG) since the last reset."""
         _check(lib().lola_state_check(self.handle, _stream(stream)))
 
     def reset(self, stream=None) -> None:
