@@ -280,7 +280,7 @@ def cross_attention(q, k, v, kv_len=None, scale=None, y=None, lse=None, workspac
     Every query of sequence b reads the keys s < kv_len[b] (int32 [B] on the device; all S if
     None).  scale is 1/sqrt(d) if None; a number or a 0-d tensor, read when the call is made.  Any
     strides with contiguous heads, a batch stride of 0 among them (one encoder output for all
-    sequences, read once for the batch if kv_len is None).  lse (float32 [B,T,Hq]), if given,
+    sequences, read as a shared prefix is if kv_len is None).  lse (float32 [B,T,Hq]), if given,
     receives each row's log-sum-exp.  workspace: scratch to use instead of an allocation
     (attention_workspace bytes); calls that may overlap need one each.  Forward only: y carries no
     gradient, whatever the inputs require."""
